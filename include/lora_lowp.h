@@ -386,6 +386,123 @@ lora_status lora_backward(const uint16_t* x, const uint16_t* dy, const float* t,
  * 4 bytes).  0 for sizes or adapter counts lora_backward does not accept. */
 size_t lora_backward_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t n_adapters, int32_t r_max);
 
+/* ---- The attention block between a decoder layer's QKV and output projections ----
+ * The QKV projection writes rows of n_q query heads, n_kv key heads and n_kv value heads of D
+ * values each.  These calls take those rows to the attention's output: norms of the query and
+ * key heads with the rotation by position (lora_qk_norm_rope, and its backward, whose result
+ * is the dY of lora_backward), the same on the way into a paged cache (lora_rope_append_kv),
+ * and attention over that cache for the tokens just appended, as a tree of drafted tokens or
+ * in order (lora_tree_attention).
+ *
+ * Limits: 0 <= T <= 65536 (T == 0 is a no-op), D in {64, 128, 256}, 1 <= n_q, n_kv <= 1024;
+ * rows may be strided (ld, in values, a multiple of 8 and at least the row's width) and are
+ * 16-byte aligned.  Data errors found on the device set bits of *status (device int32 or NULL;
+ * OR-ed in, never cleared): */
+enum {
+  LORA_ATTN_BAD_POSITION = 1, /* a position outside [0, max_pos)                         */
+  LORA_ATTN_BAD_SLOT = 2,     /* a slot past the cache's end                             */
+  LORA_ATTN_BAD_PAGE = 4,     /* a page id outside [0, n_pages)                          */
+  LORA_ATTN_BAD_LENGTH = 8,   /* q_indptr or kv_len that do not fit each other or the call */
+  LORA_ATTN_BAD_PARENT = 16   /* a parent that does not come before its child            */
+};
+
+/* Format of a paged cache: k_cache and v_cache [n_pages][n_kv][page_size][D], bf16, or e4m3fn
+ * codes with one fp32 scale a kv head (k_scale, v_scale [n_kv], positive; value = scale * code).
+ * page_size a power of two in 16 .. 1024; n_pages * page_size < 2^31; 16-byte aligned. */
+enum { LORA_KV_BF16 = 0, LORA_KV_FP8_E4M3 = 1 };
+
+/* Norm of every query and key head and rotation by position, in one pass:
+ *     n_d = x_d w_d / sqrt(mean(x^2) + eps)
+ *     y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin   for each rotated pair (a, b)
+ *  - qkv bf16 [T] rows of (n_q + 2 n_kv) D values (stride ld); the value heads are not read;
+ *  - positions int32 [T]; cos_sin float [max_pos][rot]: the rot / 2 cosines of a position, then
+ *    its sines.  Pair i of the first rot values is (i, i + rot / 2), or (2 i, 2 i + 1) with
+ *    interleaved = 1; values from rot on are not rotated.  rot a multiple of 16, 0 <= rot <= D
+ *    (0: no rotation; positions and cos_sin may be NULL);
+ *  - q_weight, k_weight float [D], or both NULL: no norm;
+ *  - q_out bf16 [T] rows of n_q D (stride ldq), k_out of n_kv D (stride ldk).  They may be the
+ *    rows' own places in qkv (q_out = qkv, k_out = qkv + n_q D, ldq = ldk = ld); any other
+ *    overlap is not allowed.
+ * Arithmetic in fp32, rounded once.  A token whose position is outside the table gets zeros. */
+lora_status lora_qk_norm_rope(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t T, int32_t n_q,
+                              int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                              int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                              uint16_t* q_out, int64_t ldq, uint16_t* k_out, int64_t ldk, int32_t* status,
+                              void* stream);
+
+/* Gradients of lora_qk_norm_rope: from dq bf16 [T][n_q D] and dk bf16 [T][n_kv D] (dense) to
+ * dqkv bf16 [T] rows (stride ldd) and, with weights, dq_weight and dk_weight float [D] (written,
+ * not accumulated into; zero for T == 0).  With g the rotation by minus the position of dy and
+ * xh = x / sqrt(mean(x^2) + eps):  dw_d = sum g_d xh_d,  dx = (g w - xh mean(g w xh)) xh / x.
+ *  - dv bf16 [T][n_kv D] is copied to the value heads' places of dqkv; NULL: they are not
+ *    written (a caller may have the attention's backward write them there);
+ *  - qkv: the forward's input (NULL without weights: it is not read); it may not overlap dqkv;
+ *  - workspace: lora_qk_norm_rope_backward_workspace_bytes(T, D) bytes with weights (partial
+ *    sums, added in a fixed order: the result does not depend on timing).
+ * A token whose position is outside the table gets zeros and adds nothing to the weights'. */
+lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, const uint16_t* dq,
+                                       const uint16_t* dk, const uint16_t* dv, int32_t T, int32_t n_q, int32_t n_kv,
+                                       int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                                       int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                                       uint16_t* dqkv, int64_t ldd, float* dq_weight, float* dk_weight,
+                                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_qk_norm_rope_backward with weights; 0 for sizes it does not accept. */
+size_t lora_qk_norm_rope_backward_workspace_bytes(int32_t T, int32_t D);
+
+/* Keys and values into a paged cache, the rotation (and with weights the norm) of
+ * lora_qk_norm_rope applied on the way; the queries, treated alike, go to q_out.
+ *  - slots int32 [T]: token t's place in the cache, page * page_size + offset; negative: its
+ *    keys and values are not stored (its queries are still written).  Two tokens of a call may
+ *    not share a slot;
+ *  - kv_fmt LORA_KV_BF16 or LORA_KV_FP8_E4M3 (k_scale and v_scale; code = e4m3(x * (1 / scale)),
+ *    to nearest even, saturated at +-448, NaN kept); values are stored unrotated.
+ * A token whose position is outside the table, or its slot past the cache, is not stored. */
+lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* positions, const int32_t* slots,
+                                int32_t T, int32_t n_q, int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos,
+                                int32_t rot, int32_t interleaved, const float* q_weight, const float* k_weight,
+                                float eps, uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache, void* v_cache,
+                                const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                                int32_t* status, void* stream);
+
+/* Masks of drafted trees from their parents: parents int32 [T] (index of a token's parent
+ * among its own sequence's drafted tokens, before its own; negative: the token follows the
+ * cached prefix), q_indptr int32 [B + 1] as below -> mask uint64 [T][words], bit i % 64 of word
+ * i / 64 set for the token itself and its ancestors.  max_q <= 64 words, words <= 16. */
+lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t B, int32_t T, int32_t max_q,
+                           int32_t words, uint64_t* mask, int32_t* status, void* stream);
+
+/* Attention over a paged cache for the tokens just appended to it.
+ *     out[t] = sum_k softmax_k(scale q[t] . K[k]) V[k]  over the keys k that token t sees
+ * Sequence b has kv_len[b] tokens in the cache, in the pages page_table[b][0 ..) in order (the
+ * last one may be part filled); the last n_b = q_indptr[b + 1] - q_indptr[b] of them are its
+ * drafted tokens, rows q_indptr[b] .. of q.  A token sees every key before the drafted ones
+ * and those drafted keys i < n_b whose bit i is set in its row of tree_mask; without a mask
+ * (NULL), those up to itself (one token: plain decode; more: a chunk of a prompt).
+ *  - q bf16 [T] rows of n_q D (stride ldq); query heads h n_q / n_kv .. share kv head h
+ *    (n_q % n_kv == 0);
+ *  - page_table int32 [B][max_pages], kv_len int32 [B], q_indptr int32 [B + 1] (ascending, from
+ *    0 to T), max_q at least every n_b; B <= 4096;
+ *  - tree_mask uint64 [T][mask_words], max_q <= 64 mask_words, mask_words <= 16;
+ *  - out bf16 [T][n_q D]; lse float [T][n_q] or NULL: the natural logarithm of the sum of
+ *    exponentials.  A row that sees nothing gets out 0 and lse -inf;
+ *  - workspace: lora_tree_attention_workspace_bytes bytes, in any state (partial results, joined
+ *    in a fixed order: the result does not depend on timing).
+ * What the cache holds in keys that a token does not see, NaN included, does not reach it.
+ * Keys in pages outside [0, n_pages) count as not seen; a sequence whose n_b is outside
+ * [0, max_q] or reaches past T is left out; one whose kv_len is below n_b or past its pages is
+ * taken as empty. */
+lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale, int32_t n_pages,
+                                int32_t page_size, const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,
+                                const int32_t* q_indptr, int32_t B, int32_t T, int32_t max_q, int32_t n_q, int32_t n_kv,
+                                int32_t D, const uint64_t* tree_mask, int32_t mask_words, float scale, uint16_t* out,
+                                float* lse, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_tree_attention: they do not depend on the number of sequences or
+ * their lengths.  0 for heads it does not accept. */
+size_t lora_tree_attention_workspace_bytes(int32_t n_q, int32_t n_kv, int32_t D, int32_t max_q);
+
 /* Device-side status word of the layer calls on this workspace since it was last
  * initialised (bits accumulate): copies one int32 to *status_dev (device pointer) on
  * `stream`.  0 = fine; bit 0 = a bounded wait in the fused launch gave up (the output

@@ -17,6 +17,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "lora_lowp.h")
 _lib = None
 
 c_i32, c_u32, c_size, c_vp = ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_void_p
+c_i64, c_f32 = ctypes.c_int64, ctypes.c_float
 
 _SIGNATURES = {
     "lora_status_string": (ctypes.c_char_p, [c_i32]),
@@ -46,6 +47,19 @@ _SIGNATURES = {
     "lora_merged_layer": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
                                   c_i32, c_vp, c_vp]),
     "lora_pack_adapter": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "lora_qk_norm_rope": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp,
+                                  c_f32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "lora_qk_norm_rope_backward": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32,
+                                           c_i32, c_i32, c_vp, c_vp, c_f32, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_size,
+                                           c_vp]),
+    "lora_qk_norm_rope_backward_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "lora_rope_append_kv": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32, c_vp,
+                                    c_vp, c_f32, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp]),
+    "lora_tree_mask": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "lora_tree_attention": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                    c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_f32, c_vp, c_vp, c_vp,
+                                    c_vp, c_size, c_vp]),
+    "lora_tree_attention_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32]),
     "lora_plan_info": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i32), c_i32]),
 }
 

@@ -17,6 +17,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_lowp.so")
 SOURCES = ["lora_kernels.hip", "lora_gemm_pf.hip", "lora_backward.hip", "lora_api.cpp"]
+# the attention block, apart from the layer's sources (whose hash names the layer's profiles)
+CSRC_ATTN = os.path.join(HERE, "csrc_attn")
+SOURCES_ATTN = ["rope_kernels.hip", "tree_attention.hip", "attn_api.cpp"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops off: no v_pk_{add,mul,fma}_f32 in the device code.
@@ -58,7 +61,8 @@ def hipcc() -> str:
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
+    cmd = [hipcc(), *FLAGS, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES],
+           *[os.path.join(CSRC_ATTN, s) for s in SOURCES_ATTN]]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
