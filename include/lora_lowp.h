@@ -481,11 +481,11 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
  * (NULL), those up to itself (one token: plain decode; more: a chunk of a prompt).
  *  - q bf16 [T] rows of n_q D (stride ldq); query heads h n_q / n_kv .. share kv head h
  *    (n_q % n_kv == 0);
- *  - page_table int32 [B][max_pages], kv_len int32 [B], q_indptr int32 [B + 1] (ascending, from
+ *  - page_table int32 [B][max_pages] (max_pages * page_size <= 2^30), kv_len int32 [B], q_indptr int32 [B + 1] (ascending, from
  *    0 to T), max_q at least every n_b; B <= 4096;
  *  - tree_mask uint64 [T][mask_words], max_q <= 64 mask_words, mask_words <= 16;
  *  - out bf16 [T][n_q D]; lse float [T][n_q] or NULL: the natural logarithm of the sum of
- *    exponentials.  A row that sees nothing gets out 0 and lse -inf;
+ *    exponentials.  A row that sees nothing (or only scores of -inf) gets out 0, lse -inf;
  *  - workspace: lora_tree_attention_workspace_bytes bytes, in any state (partial results, joined
  *    in a fixed order: the result does not depend on timing).
  * What the cache holds in keys that a token does not see, NaN included, does not reach it.

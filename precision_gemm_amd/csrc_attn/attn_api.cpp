@@ -176,7 +176,7 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   if (!cache_fmt_ok(kv_fmt) || B < 0 || max_q < 0 || max_pages < 0 || n_q % n_kv != 0 || !isfinite(scale))
     return LORA_ERR_INVALID_ARG;
   if ((st = check_pages(n_pages, page_size, n_kv, &lg)) != LORA_OK) return st;
-  if (B > ATTN_MAX_B || max_q > MAX_TOKENS || (int64_t)max_pages * page_size > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  if (B > ATTN_MAX_B || max_q > MAX_TOKENS || (int64_t)max_pages * page_size > (1 << 30)) return LORA_ERR_UNSUPPORTED;
   if (tree_mask) {
     if (mask_words < 1) return LORA_ERR_INVALID_ARG;
     if (mask_words > MAX_DRAFT_WORDS || max_q > 64 * mask_words) return LORA_ERR_UNSUPPORTED;

@@ -52,6 +52,17 @@ __device__ __forceinline__ int q_place(int s, int g) {
   return FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
 }
 
+// A table entry at an address that is the same for the whole wave, through the scalar cache
+// (the call's index tables are not written while it runs).
+__device__ __forceinline__ int ld_table(const int* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(4))) const int c_int;
+  return *(c_int*)(reinterpret_cast<uintptr_t>(p));
+#else
+  return *p;  // host pass only; never executed
+#endif
+}
+
 template <int BYTES>
 __device__ __forceinline__ void ldg_words(const char* p, uint32_t* w) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -93,15 +104,14 @@ __device__ __forceinline__ uint32_t visible8(const uint64_t* mrow, int words, in
 
 // One sequence: its queries and keys, and how many units and steps they make.
 struct Seq { int q0, n, kv, steps, blocks; bool bad; };
-__device__ __forceinline__ Seq read_seq(const TreeAttnParams& p, int b, int block_rows) {
+__device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1, int kv, int block_rows) {
   Seq s;
-  s.q0 = p.q_indptr[b];
-  const int q1 = p.q_indptr[b + 1];
-  s.kv = p.kv_len[b];
+  s.q0 = q0;
+  s.kv = kv;
   s.bad = false;
-  s.n = q1 - s.q0;
-  if (s.q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = true; }
-  if (s.kv < s.n || (long)s.kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = true; }
+  s.n = q1 - q0;
+  if (q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = true; }
+  if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = true; }
   s.steps = max(1, (s.kv + ATTN_KEYS - 1) / ATTN_KEYS);
   s.blocks = (s.n * p.group + block_rows - 1) / block_rows;
   return s;
@@ -114,7 +124,7 @@ __device__ __forceinline__ void work_prefix(const TreeAttnParams& p, int block_r
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < p.B) {
-      const Seq s = read_seq(p, b, block_rows);
+      const Seq s = make_seq(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
       if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
       mine += p.n_kv * s.blocks * s.steps;
       cum[b + 1] = mine;
@@ -138,6 +148,18 @@ __device__ __forceinline__ void work_prefix(const TreeAttnParams& p, int block_r
   __syncthreads();
 }
 
+// Write one finished row: four values of out and, once, lse.  No key seen: L is 0, else it is
+// at least 1 (the score that set m), or not a number.
+template <int D>
+__device__ __forceinline__ void put_row(const TreeAttnParams& p, int q0, int h, int r, int c4, const float4& a, float M, float L,
+                                        float vs) {
+  const float inv = L == 0.f ? 0.f : vs / L;
+  const int j = r / p.group;
+  const long at = (long)(q0 + j) * p.n_q + h * p.group + (r - j * p.group);
+  *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) = make_uint2(bf16x2_rne(a.x * inv, a.y * inv), bf16x2_rne(a.z * inv, a.w * inv));
+  if (c4 == 0 && p.lse) p.lse[at] = L == 0.f ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+}
+
 template <int D, int RT, bool FP8, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   using G = Geo<D, FP8>;
@@ -145,7 +167,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   constexpr int OS = D + 4;        // row stride of the joining buffer (floats)
   __shared__ __attribute__((aligned(16))) float so[4 * 16 * OS];
   __shared__ float sml[4][RT * 16][2];
-  __shared__ int wave_sum[4];
+  __shared__ int wave_sum[4], first_seq;
   // heads of 256: the queries are kept in LDS as operands, their registers hold keys and values
   constexpr bool Q_LDS = D == 256;
   static_assert(!Q_LDS || RT == 1, "one row tile in LDS");
@@ -166,15 +188,10 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   if (tid == 0) p.desc[4 * wg] = 0;
   if (cur >= end) return;
 
-  int b = 0;
-  {  // last sequence that begins at or before cur
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= cur) lo = mid; else hi = mid;
-    }
-    b = __builtin_amdgcn_readfirstlane(lo);
-  }
+  for (int c = tid; c < p.B; c += 256)
+    if (cum[c] <= cur && cur < cum[c + 1]) first_seq = c;
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(first_seq);
   cur = __builtin_amdgcn_readfirstlane(cur);
 
   const int page = 1 << p.page_log2;
@@ -184,7 +201,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   while (cur < end) {
     while (cum[b + 1] <= cur) ++b;  // skips sequences without queries
     b = __builtin_amdgcn_readfirstlane(b);
-    const Seq sq = read_seq(p, b, RT * 16);
+    const Seq sq = make_seq(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), RT * 16);
     const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
     const int unit = local / sq.steps, t0 = local - unit * sq.steps;
     const int t1 = min(sq.steps, t0 + end - cur);
@@ -226,8 +243,8 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
     // this wave's step: keys key0 .. key0 + 31 in two halves of 16, each within one page
     auto lookup = [&](int key0, int& p0, int& p1) {
       const int last = (kv - 1) >> p.page_log2;
-      p0 = table[min(key0 >> p.page_log2, last)];
-      p1 = table[min((key0 + 16) >> p.page_log2, last)];
+      p0 = ld_table(table + min(key0 >> p.page_log2, last));
+      p1 = ld_table(table + min((key0 + 16) >> p.page_log2, last));
     };
     auto row_base = [&](int id, int key) {  // byte offset of the half's first row
       const int ok = (unsigned)id < (unsigned)p.n_pages ? id : 0;
@@ -263,10 +280,11 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       }
     };
     int key0 = t0 * ATTN_KEYS + wave * 32;
-    int id0 = 0, id1 = 0;
+    int id0 = 0, id1 = 0, n0 = 0, n1 = 0;  // pages of this step and of the next one
     long b0 = 0, b1 = 0;
     if (key0 < kv) {
       lookup(key0, id0, id1);
+      lookup(key0 + ATTN_KEYS, n0, n1);
       b0 = row_base(id0, key0);
       b1 = row_base(id1, key0 + 16);
       load_k(b0, b1);
@@ -413,19 +431,15 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       if (key0 >= kv) break;  // the last step's tail: nothing for this wave
       const int next = key0 + ATTN_KEYS;
       const bool more = t + 1 < t1 && next < kv;
-      int n0 = 0, n1 = 0;
-      long nb0 = 0, nb1 = 0;
-      if (more) {
-        lookup(next, n0, n1);
-        nb0 = row_base(n0, next);
-        nb1 = row_base(n1, next + 16);
-      }
+      const long nb0 = row_base(n0, next), nb1 = row_base(n1, next + 16);
+      int f0, f1;
+      lookup(next + ATTN_KEYS, f0, f1);
       const bool bad0 = (unsigned)id0 >= (unsigned)p.n_pages, bad1 = (unsigned)id1 >= (unsigned)p.n_pages;
       if (key0 + 32 > prefix || bad0 || bad1)
         step(std::true_type{}, more, nb0, nb1, bad0, bad1);
       else
         step(std::false_type{}, more, nb0, nb1, false, false);
-      id0 = n0; id1 = n1; b0 = nb0; b1 = nb1;
+      id0 = n0; id1 = n1; n0 = f0; n1 = f1; b0 = nb0; b1 = nb1;
     }
 
     // join the four waves
@@ -470,16 +484,12 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const float mw = sml[w][rt * 16 + row][0];
-            L += mw == NEG_INF ? 0.f : sml[w][rt * 16 + row][1] * __builtin_amdgcn_exp2f(mw - M);
+            L += sml[w][rt * 16 + row][1] * (mw == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(mw - M));
             const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + row) * OS + 4 * c4);
             a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
           }
           if (whole) {
-            const float inv = M == NEG_INF ? 0.f : vs / L;
-            const int j = r / p.group;
-            const long at = (long)(sq.q0 + j) * p.n_q + h * p.group + (r - j * p.group);
-            *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) = make_uint2(bf16x2_rne(a.x * inv, a.y * inv), bf16x2_rne(a.z * inv, a.w * inv));
-            if (c4 == 0 && p.lse) p.lse[at] = M == NEG_INF ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+            put_row<D>(p, sq.q0, h, r, c4, a, M, L, vs);
           } else {
             const long at = (long)slot * (RT * 16) + rt * 16 + row;
             *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c4) = a;
@@ -523,7 +533,7 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
     const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * c4);
     const float f = ml.x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml.x - M);
-    L += ml.x == NEG_INF ? 0.f : ml.y * f;
+    L += ml.y * f;
     a.x += v.x * f; a.y += v.y * f; a.z += v.z * f; a.w += v.w * f;
   }
 #pragma unroll
@@ -533,11 +543,7 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
   }
   if (pg) return;
   const float vs = p.v_scale ? p.v_scale[ds.z] : 1.f;
-  const float inv = M == NEG_INF ? 0.f : vs / L;
-  const int j = r / p.group;
-  const long at = (long)(q0 + j) * p.n_q + ds.z * p.group + (r - j * p.group);
-  *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) = make_uint2(bf16x2_rne(a.x * inv, a.y * inv), bf16x2_rne(a.z * inv, a.w * inv));
-  if (c4 == 0 && p.lse) p.lse[at] = M == NEG_INF ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+  put_row<D>(p, q0, ds.z, r, c4, a, M, L, vs);
 }
 
 // Bit i of row t: drafted token i is t or one of its ancestors.  One thread a token; a parent

@@ -426,6 +426,7 @@ ATTN = [  # ns, kvs, n_q, n_kv, D, page, mask
     ([4, 2], [900, 65], 8, 2, 256, 32, "tree"),
     ([40, 1], [45, 300], 15, 3, 256, 16, "any"),
     ([1], [40000], 16, 2, 128, 1024, "none"),
+    ([2, 1], [90000, 70], 8, 1, 64, 16, "none"),
     ([1] * 300, [1 + (37 * b) % 90 for b in range(300)], 2, 1, 64, 16, "none"),
 ]
 
@@ -491,6 +492,17 @@ def test_attention_empty_rows_and_large_scores():
     assert torch.equal(out[rows], keep[0][rows]) and not torch.isfinite(lse[6, 1]) and torch.equal(out[6, [0, 2, 3]], keep[0][6, [0, 2, 3]])
 
 
+def test_attention_rows_of_nan():
+    """A row that sees only keys that are not numbers is NaN, not empty."""
+    torch = _torch()
+    print("[case] rows of NaN", flush=True)
+    b = Batch(16, [2], [2], 2, 1, 64, 16, False, "any")
+    b.masks = [1, 2]
+    b.k[b.table[0, 0], :, 1] = float("nan")
+    out, lse = b.run()
+    assert torch.isfinite(out[0]).all() and torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+
+
 def test_attention_data_errors():
     torch = _torch()
     import precision_gemm_amd as P
@@ -538,20 +550,29 @@ def test_attention_data_errors():
 
 
 def test_attention_same_bits_whatever_the_workspace():
-    """Bitwise the same again, with a workspace of any content, on another stream, and with any
-    sequences beside it that leave the split of the keys as it was."""
+    """Bitwise the same again, whatever the workspace holds, on another stream, and with any mask
+    bits past a sequence's tokens."""
     torch = _torch()
     import precision_gemm_amd as P
     print("[case] workspace, stream", flush=True)
     b = Batch(12, [3, 1, 5], [3000, 900, 100], 8, 2, 128, 32, False, "tree")
     want = b.run()
     b.check(*want)
-    n = P.tree_attention_workspace_bytes(8, 2, 128, 5)
     for fill in (0, 255):
-        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        ws = torch.full((P.tree_attention_workspace_bytes(8, 2, 128, 5),), fill, dtype=torch.uint8, device="cuda")
         out, lse = torch.full_like(want[0], float("nan")), torch.full_like(want[1], float("nan"))
         got = b.run(workspace=ws, out=out, lse=lse)
         assert got[0] is out and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    # one workspace for calls of different heads, lengths and numbers of rows
+    big = torch.full((96 << 20,), 255, dtype=torch.uint8, device="cuda")
+    others = [Batch(20 + i, ns, kvs, n_q, n_kv, D, 16, False) for i, (ns, kvs, n_q, n_kv, D) in enumerate([
+        ([1], [30000], 4, 1, 64), ([40, 1], [700, 5000], 8, 1, 128), ([3], [9000], 2, 1, 256), ([1] * 9, [2000] * 9, 8, 8, 128)])]
+    alone = [o.run() for o in others]
+    for _ in range(2):
+        for o, (a, l) in zip(others, alone):
+            got = o.run(workspace=big)
+            assert torch.equal(got[0], a) and torch.equal(got[1], l)
+    others[0].check(*alone[0])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
