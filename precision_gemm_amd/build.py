@@ -1,4 +1,5 @@
-"""Build the HIP library ``liblora_lowp.so`` in-tree for gfx950 with hipcc.
+"""Build the HIP library ``liblora_lowp.so`` in-tree for gfx950 with hipcc, and the attention
+block's Python binding ``_attn.so`` that links to it.
 
 Run as ``python -m precision_gemm_amd.build``; ``__graft_entry__.build()`` calls
 :func:`build`.  Every call compiles (no up-to-date check), so a changed source is
@@ -34,6 +35,7 @@ FLAGS = [
     "-Rpass-analysis=kernel-resource-usage",
 ]
 RESOURCES = LIB + ".resources.json"
+BINDING = os.path.join(HERE, "_attn.so")
 
 
 def parse_resources(stderr: str) -> dict:
@@ -76,7 +78,30 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     with open(RESOURCES, "w") as f:
         json.dump(parse_resources(res.stderr), f, indent=1, sort_keys=True)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The attention block's binding (host code against the installed torch), beside the library
+    it calls."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{p}" for p in include_paths()], "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC_ATTN, "binding.cpp"), "-o", tmp, f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding's compilation failed ({res.returncode}):\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def resources() -> dict:
