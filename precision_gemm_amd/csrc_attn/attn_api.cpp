@@ -59,6 +59,10 @@ RopeParams rope_params(const uint16_t* qkv, int64_t ld, const int32_t* positions
   return p;
 }
 
+inline size_t plan_bytes(const TreeAttnPlan& pl) {
+  return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
+}
+
 inline int bwd_wgs(int32_t T) { return T < 4 * ROPE_BWD_WGS ? (T + 3) / 4 : ROPE_BWD_WGS; }
 
 }  // namespace
@@ -160,8 +164,12 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
 size_t lora_tree_attention_workspace_bytes(int32_t n_q, int32_t n_kv, int32_t D, int32_t max_q) {
   if (check_heads(1, n_q, n_kv, D) != LORA_OK || n_q % n_kv != 0 || max_q < 1 || max_q > MAX_TOKENS) return 0;
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
-  const TreeAttnPlan pl = tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows);
-  return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
+  size_t most = 0;  // of the two cache formats
+  for (int fp8 = 0; fp8 < 2; ++fp8) {
+    const size_t n = plan_bytes(tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows, fp8));
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, const void* k_cache,
@@ -191,12 +199,12 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))) return LORA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
   if (rows > INT32_MAX / 2) return LORA_ERR_UNSUPPORTED;
-  const TreeAttnPlan pl = tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows);
+  const TreeAttnPlan pl = tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows, fp8);
   // all steps of a call are numbered in 32 bits
-  const double steps = (double)B * n_kv * (double)((rows + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles)) *
-                       ((double)max_pages * page_size / ATTN_KEYS + 1.0);
+  const double steps = (double)B * n_kv * (double)((rows + pl.block_rows - 1) / pl.block_rows) *
+                       ((double)max_pages * page_size / (pl.shared ? ATTN_SHARED_KEYS : ATTN_KEYS) + 1.0);
   if (steps > 2.0e9) return LORA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_tree_attention_workspace_bytes(n_q, n_kv, D, max_q))
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < plan_bytes(pl))
     return LORA_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
   TreeAttnParams p{};

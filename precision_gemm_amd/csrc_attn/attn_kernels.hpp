@@ -73,7 +73,7 @@ struct TreeAttnParams {
   float scale_log2;        // the softmax scale times log2(e)
   uint16_t* out;           // bf16 [T][n_q][D]
   float* lse;              // [T][n_q], may be null
-  int* desc;               // [n_wg][4]: a unit that this workgroup began and others end
+  int* desc;               // [n_wg][ATTN_DESC]: a unit that this workgroup began and others end
   float* part_ml;          // [2 n_wg][rows][2]
   float* part_o;           // [2 n_wg][rows][D]
   int n_wg;
@@ -81,11 +81,16 @@ struct TreeAttnParams {
 };
 
 constexpr int ATTN_MAX_B = 4096;     // sequences of one call (their prefix sums live in LDS)
-constexpr int ATTN_KEYS = 128;       // keys of one workgroup step: 32 for each of four waves
+constexpr int ATTN_DESC = 8;         // words of a cut unit's description
+constexpr int ATTN_GROUP = 32;       // keys of one MFMA group
+constexpr int ATTN_SHARED_KEYS = 64; // keys of a step of two row tiles a wave
+constexpr int ATTN_KEYS = 128;       // keys of a workgroup step where waves split them: a group for each of four
 
-// Row tiles of 16 queries a workgroup holds, and its launch's workgroups.
-struct TreeAttnPlan { int row_tiles, n_wg; size_t desc_bytes, ml_bytes, o_bytes; };
-TreeAttnPlan tree_attn_plan(int D, int rows);
+// How a call's rows (drafted tokens times query heads of a kv head) are taken: by waves that
+// split a step's keys, or (`shared`) that share them; row tiles of 16 a wave holds, rows of a
+// workgroup, workgroups.
+struct TreeAttnPlan { bool shared; int row_tiles, block_rows, n_wg; size_t desc_bytes, ml_bytes, o_bytes; };
+TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8);
 hipError_t launch_tree_attention(const TreeAttnParams& p, const TreeAttnPlan& pl, int D, bool fp8, hipStream_t s);
 hipError_t launch_tree_mask(const int* parents, const int* q_indptr, int B, int T, int max_q, int words, uint64_t* mask,
                             int* status, hipStream_t s);

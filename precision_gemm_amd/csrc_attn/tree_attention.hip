@@ -8,10 +8,10 @@
 // by 2^8 (the sums are in 32 bits, so exp(S - m) <= 2^8 costs nothing), which takes the
 // rescaling and the maximum's exchange between lanes out of almost every step.
 //
-// Split: the keys of all (sequence, kv head, row block) units form one line of steps of 128
-// keys; every workgroup takes an equal stretch of it, whatever the sequences' lengths, and
-// finds its place from a prefix sum over the sequences that it computes itself, so the host
-// needs no lengths.  A unit cut between workgroups leaves its pieces (m, l, unnormalised O in
+// Split: the keys of all (sequence, kv head, row block) units form one line of steps; a
+// workgroup's stretch of it is found, whatever the sequences' lengths, from a prefix sum over
+// the sequences that every workgroup computes itself (find_stretch), so the host needs no
+// lengths.  A unit cut between workgroups leaves its pieces (m, l, unnormalised O in
 // 32 bits) in the workspace; k_tree_combine joins them in order.
 //
 // Layout: a wave takes 32 keys of a step and all rows of its unit (the query heads that share
@@ -63,6 +63,10 @@ __device__ __forceinline__ int ld_table(const int* p) {
 #endif
 }
 
+__device__ __forceinline__ uint4 signed_q(const uint4& v, uint32_t flip) {
+  return make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+}
+
 template <int BYTES>
 __device__ __forceinline__ void ldg_words(const char* p, uint32_t* w) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -104,6 +108,7 @@ __device__ __forceinline__ uint32_t visible8(const uint64_t* mrow, int words, in
 
 // One sequence: its queries and keys, and how many units and steps they make.
 struct Seq { int q0, n, kv, steps, blocks; bool bad; };
+template <int KEYS>
 __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1, int kv, int block_rows) {
   Seq s;
   s.q0 = q0;
@@ -112,40 +117,250 @@ __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1,
   s.n = q1 - q0;
   if (q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = true; }
   if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = true; }
-  s.steps = max(1, (s.kv + ATTN_KEYS - 1) / ATTN_KEYS);
+  s.steps = max(1, (s.kv + KEYS - 1) / KEYS);
   s.blocks = (s.n * p.group + block_rows - 1) / block_rows;
   return s;
 }
 
-// Prefix sum of the sequences' work in LDS: cum[b] steps before sequence b, cum[B] in all.
-__device__ __forceinline__ void work_prefix(const TreeAttnParams& p, int block_rows, int* cum, int* wave_sum) {
-  const int tid = threadIdx.x, lane = tid & 63, per = (p.B + 255) / 256;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
+// Sum of a value over the workgroup's threads, in every thread (THREADS / 64 words of LDS); and
+// the sum over the threads before this one.
+template <int THREADS>
+__device__ __forceinline__ int2 group_scan(int v, int* wave_sum) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(incl, d);
+    if (lane >= d) incl += u;
+  }
+  __syncthreads();  // an earlier scan's sums are read
+  if (lane == 63) wave_sum[wave] = incl;
+  __syncthreads();
+  int before = incl - v, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    const int u = wave_sum[w];
+    before += w < wave ? u : 0;
+    total += u;
+  }
+  return make_int2(before, total);
+}
+
+// A workgroup's stretch [cur, end) of the line of all units' steps, and the sequence it begins
+// in, found from a prefix sum over the sequences' work that leaves cum[b], the steps before
+// sequence b, in LDS.
+//  - All workgroups take equal stretches of `per` steps, wherever those cut the units
+//    (pieces = 0).
+//  - EVEN, where the units are no more than the workgroups and it makes no piece over 1.5 times
+//    as long: every unit is cut evenly, into as many pieces (`pieces`) as keep the longest
+//    piece shortest with a workgroup each.  Nobody begins a second unit, and most write one
+//    piece, not two (256 rows of 128 values are 128 KB): trees of up to 64 tokens 39 us against
+//    46, but its search costs a few scans: trees of up to 16 tokens 21.5 us against 18.9.
+struct Stretch { int cur, end, b, per, pieces; };
+template <int THREADS, int KEYS, bool EVEN>
+__device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int* wave_sum,
+                                                Stretch* found) {
+  const int tid = threadIdx.x, each = (p.B + THREADS - 1) / THREADS;
+  int mine = 0, units = 0, steps = 1;
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
     if (b < p.B) {
-      const Seq s = make_seq(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
+      const Seq s = make_seq<KEYS>(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
       if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
+      units += p.n_kv * s.blocks;
+      steps = s.steps;
       mine += p.n_kv * s.blocks * s.steps;
       cum[b + 1] = mine;
     }
   }
-  int incl = mine;
+  const int2 work = group_scan<THREADS>(mine, wave_sum);
+  bool even = EVEN && each == 1 && group_scan<THREADS>(min(units, 1 << 20), wave_sum).y <= p.n_wg;
+  if (tid == 0) {
+    cum[0] = 0;
+    found->cur = found->end = 0;
+  }
+  Stretch r;
+  int lo = max(1, (work.y + p.n_wg - 1) / p.n_wg), hi = lo + lo / 2;
+  int2 at;
+  if (even) {
+    at = group_scan<THREADS>(units * ((steps + hi - 1) / hi), wave_sum);
+    even = at.y <= p.n_wg;
+  }
+  if (even) {
+    const int b = tid;
+    // the least c for which pieces of at most c steps are no more than the workgroups
+    while (lo < hi) {
+      const int c = (lo + hi) >> 1;
+      const int2 t = group_scan<THREADS>(units * ((steps + c - 1) / c), wave_sum);
+      if (t.y <= p.n_wg) { hi = c; at = t; } else { lo = c + 1; }
+    }
+    const int k = (steps + hi - 1) / hi;
+    if (b < p.B) {
+      cum[b + 1] += work.x;
+      if (at.x <= wg && wg < at.x + units * k) {
+        const int unit = (wg - at.x) / k, piece = wg - at.x - unit * k;
+        const int base = work.x + unit * steps;
+        *found = Stretch{base + (int)((long)steps * piece / k), base + (int)((long)steps * (piece + 1) / k), b, 1, k};
+      }
+    }
+  } else {
+    r.per = (work.y + p.n_wg - 1) / p.n_wg;
+    r.cur = min(work.y, wg * r.per);
+    r.end = min(work.y, r.cur + r.per);
+    int from = work.x;
+    for (int i = 0; i < each; ++i) {
+      const int b = tid * each + i;
+      if (b < p.B) {
+        const int next = work.x + cum[b + 1];
+        if (from <= r.cur && r.cur < next) *found = Stretch{r.cur, r.end, b, r.per, 0};
+        cum[b + 1] = next;
+        from = next;
+      }
+    }
+  }
+  __syncthreads();
+  r.cur = __builtin_amdgcn_readfirstlane(found->cur);
+  r.end = __builtin_amdgcn_readfirstlane(found->end);
+  r.b = __builtin_amdgcn_readfirstlane(found->b);
+  r.per = __builtin_amdgcn_readfirstlane(found->per);
+  r.pieces = __builtin_amdgcn_readfirstlane(found->pieces);
+  return r;
+}
+
+// One row tile's scores of 32 keys (S^T: lane (g, i) has keys 8 g .. 8 g + 7 of row i) into
+// the running softmax; returns the probabilities as the MFMA operand of O^T = V^T P^T.
+template <int NT, bool SPECIAL>
+__device__ __forceinline__ uint4 softmax_step(const v4f (&s)[2], float sc, uint32_t vis, float& m, float& l, v4f (&o)[NT]) {
+  float x[8];  // products of keys 8 g + e; sc >= 0 takes them to log2 units
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
+  for (int e = 0; e < 8; ++e) x[e] = SPECIAL && !((vis >> e) & 1u) ? NEG_INF : s[e >> 2][e & 3];
+  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), fmaxf(fmaxf(x[3], x[4]), fmaxf(fmaxf(x[5], x[6]), x[7]))) * sc;
+  if (__any(mx > m + SLACK)) {
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    // each row by its own scores alone: what a row gets does not depend on its neighbours
+    const bool up = mx > m + SLACK;
+    const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.f;
+    m = up ? mx : m;
+    l *= f;
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) o[tt] *= f;
   }
-  if (lane == 63) wave_sum[tid >> 6] = incl;
-  __syncthreads();
-  int before = incl - mine;
-  for (int w = 0; w < (tid >> 6); ++w) before += wave_sum[w];
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < p.B) cum[b + 1] += before;
+  const float ref = m == NEG_INF ? 0.f : m;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], sc, -ref));
+    if (SPECIAL && !((vis >> e) & 1u)) x[e] = 0.f;  // with a scale of 0, -inf * 0 is no zero
   }
-  if (tid == 0) cum[0] = 0;
-  __syncthreads();
+  l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  // P enters the MFMA in bf16 (relative error 2^-8 an element at most, as the output's own
+  // rounding); its sum l is taken before the rounding, in 32 bits
+  return make_uint4(bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7]));
+}
+
+// 8 keys x 2 values in VE-word rows -> the MFMA operand of one value: word w of the rows, its
+// low or high half by `odd`.
+template <int VE>
+__device__ __forceinline__ uint4 transposed(const uint32_t (&vb)[8][VE], int w, int odd) {
+  const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
+  return make_uint4(__builtin_amdgcn_perm(vb[1][w], vb[0][w], sel), __builtin_amdgcn_perm(vb[3][w], vb[2][w], sel),
+                    __builtin_amdgcn_perm(vb[5][w], vb[4][w], sel), __builtin_amdgcn_perm(vb[7][w], vb[6][w], sel));
+}
+
+// A lane's V words of one key, widened to bf16.
+template <typename G, bool FP8>
+__device__ __forceinline__ void widen_v(const uint32_t* in, uint32_t* out) {
+  if constexpr (FP8) {
+#pragma unroll
+    for (int w = 0; w < G::NCH * G::VW; ++w) {
+      const uint2 u = fp8x4_to_bf16(in[w]);
+      out[2 * w] = u.x;
+      out[2 * w + 1] = u.y;
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < G::NCH * G::VW; ++w) out[w] = in[w];
+  }
+}
+
+// K operand of MFMA step st from a lane's loads of 16 keys.
+template <bool FP8>
+__device__ __forceinline__ uint4 k_operand(const uint4* kr, int st) {
+  if constexpr (FP8) {
+    const uint4 w = kr[st >> 1];
+    const uint2 lo = fp8x4_to_bf16((st & 1) ? w.z : w.x), hi = fp8x4_to_bf16((st & 1) ? w.w : w.y);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  } else {
+    return kr[st];
+  }
+}
+
+// V rows (as loaded) of a group of 32 keys made safe for a product that multiplies unseen keys by zero:
+// rows of keys past the end, and of pages that do not exist, hold anything and are zeroed; a
+// drafted key that only some rows see must not reach the others through 0 * NaN, so rows with
+// values that are not finite are zeroed too, and returned (bit e: key 8 g + e of this lane's
+// group g) to be added apart, to the rows that see them (add_odd_keys).
+template <bool FP8, int W>
+__device__ __forceinline__ uint32_t clean_v(uint32_t (&row)[8][W], int g, bool gone, int d0, int n) {
+  // a value that is not finite has all its exponent bits (e4m3: all but the sign), to which
+  // adding one carries into the sign's place
+  constexpr uint32_t BITS = FP8 ? 0x7f7f7f7fu : 0x7f807f80u, ONE = FP8 ? 0x01010101u : 0x00800080u, CARRY = FP8 ? 0x80808080u : 0x80008000u;
+  uint32_t odd = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool none = gone || d0 + e >= n;
+    uint32_t carry = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      row[e][w] = none ? 0u : row[e][w];
+      carry |= (row[e][w] & BITS) + ONE;
+    }
+    const uint64_t any = __ballot((carry & CARRY) != 0);
+    if ((any >> (16 * g)) & 0xffffu) {
+      odd |= 1u << e;
+#pragma unroll
+      for (int w = 0; w < W; ++w) row[e][w] = 0u;
+    }
+  }
+  return odd;
+}
+
+// The keys that clean_v took out (bit 8 g + e of `odd`), one at a time: each as the operand
+// whose only key it is, its product added to the rows that see it.
+template <int D, bool FP8>
+__device__ __forceinline__ void add_odd_keys(uint32_t odd, const char* v0, const char* v1, const uint4& pb, uint32_t vis,
+                                             v4f (&o)[D / 16]) {
+  using G = Geo<D, FP8>;
+  constexpr int VE = G::NCH * G::CH / 2;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  for (int kk = 0; kk < 32; ++kk) {
+    if (!((odd >> kk) & 1u)) continue;
+    const int gk = kk >> 3, e = kk & 7;
+    const char* row = (gk < 2 ? v0 : v1) + (kk & 15) * G::ROWB + i * G::VB;
+    uint32_t raw[G::NCH * G::VW], v[VE];
+#pragma unroll
+    for (int c = 0; c < G::NCH; ++c) ldg_words<G::VB>(row + c * 16 * G::VB, &raw[c * G::VW]);
+    widen_v<G, FP8>(raw, v);
+    const bool sees = (__shfl((int)vis, 16 * gk + i) >> e) & 1;
+#pragma unroll
+    for (int tt = 0; tt < D / 16; ++tt) {
+      const uint32_t half = (v[tt >> 1] >> (16 * (tt & 1))) & 0xffffu;
+      const uint32_t val = g == gk ? half << (16 * (e & 1)) : 0u;
+      const uint4 a = make_uint4((e >> 1) == 0 ? val : 0u, (e >> 1) == 1 ? val : 0u, (e >> 1) == 2 ? val : 0u, (e >> 1) == 3 ? val : 0u);
+      const v4f add = mfma_bf16_16x16x32(a, pb, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[tt][r] += sees ? add[r] : 0.f;
+      __builtin_amdgcn_sched_barrier(0);  // one tile at a time: this path is rare, its registers are not
+    }
+  }
+}
+
+// What the join needs of a unit that workgroup wg began and others ended: its pieces, first
+// query row, rows, kv head and row block.
+__device__ __forceinline__ void put_desc(const TreeAttnParams& p, int wg, int pieces, const Seq& sq, int h, int rb) {
+  int4* d = reinterpret_cast<int4*>(p.desc + ATTN_DESC * wg);
+  d[0] = make_int4(pieces, sq.q0, sq.n * p.group, h);
+  d[1] = make_int4(rb, 0, 0, 0);
 }
 
 // Write one finished row: four values of out and, once, lse.  No key seen: L is 0, else it is
@@ -160,6 +375,28 @@ __device__ __forceinline__ void put_row(const TreeAttnParams& p, int q0, int h, 
   if (c4 == 0 && p.lse) p.lse[at] = L == 0.f ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
 }
 
+// Write the finished rows of a tile in the lanes' layout: lane (g, i) has row r at places
+// 16 CH c + CH (4 g + x) + e of tile c CH + e, element x.
+template <int D, int CH>
+__device__ __forceinline__ void put_tile(const TreeAttnParams& p, int q0, int rows, int h, int r, int g, const v4f (&o)[D / 16],
+                                         float M, float L, float vs) {
+  if (r >= rows) return;
+  const float inv = L == 0.f ? 0.f : vs / L;
+  const int j = r / p.group;
+  const long at = (long)(q0 + j) * p.n_q + h * p.group + (r - j * p.group);
+#pragma unroll
+  for (int c = 0; c < D / (16 * CH); ++c)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int e = 0; e < CH; e += 4) {
+        const int t = c * CH + e;
+        *reinterpret_cast<uint2*>(p.out + at * D + 16 * CH * c + CH * (4 * g + x) + e) =
+            make_uint2(bf16x2_rne(o[t][x] * inv, o[t + 1][x] * inv), bf16x2_rne(o[t + 2][x] * inv, o[t + 3][x] * inv));
+      }
+  if (g == 0 && p.lse) p.lse[at] = L == 0.f ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+}
+
 template <int D, int RT, bool FP8, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   using G = Geo<D, FP8>;
@@ -167,7 +404,8 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   constexpr int OS = D + 4;        // row stride of the joining buffer (floats)
   __shared__ __attribute__((aligned(16))) float so[4 * 16 * OS];
   __shared__ float sml[4][RT * 16][2];
-  __shared__ int wave_sum[4], first_seq;
+  __shared__ int wave_sum[4];
+  __shared__ Stretch found;
   // heads of 256: the queries are kept in LDS as operands, their registers hold keys and values
   constexpr bool Q_LDS = D == 256;
   static_assert(!Q_LDS || RT == 1, "one row tile in LDS");
@@ -180,19 +418,10 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   // neighbours, which read the same queries and (row blocks of a unit) the same keys, share an L2
   const int wg = (blockIdx.x & 7) * (p.n_wg >> 3) + (blockIdx.x >> 3);
 
-  work_prefix(p, RT * 16, cum, wave_sum);
-  const int total = cum[p.B];
-  const int per = (total + p.n_wg - 1) / p.n_wg;
-  int cur = wg * per;
-  const int end = min(total, cur + per);
-  if (tid == 0) p.desc[4 * wg] = 0;
-  if (cur >= end) return;
-
-  for (int c = tid; c < p.B; c += 256)
-    if (cum[c] <= cur && cur < cum[c + 1]) first_seq = c;
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(first_seq);
-  cur = __builtin_amdgcn_readfirstlane(cur);
+  const Stretch mine = find_stretch<256, ATTN_KEYS, false>(p, wg, RT * 16, cum, wave_sum, &found);
+  if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
+  int cur = mine.cur, b = mine.b;
+  const int end = mine.end;
 
   const int page = 1 << p.page_log2;
   const int koff = (8 * ((i >> 2) & 1) + (i & 3)) * G::ROWB + 16 * g;
@@ -201,7 +430,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   while (cur < end) {
     while (cum[b + 1] <= cur) ++b;  // skips sequences without queries
     b = __builtin_amdgcn_readfirstlane(b);
-    const Seq sq = make_seq(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), RT * 16);
+    const Seq sq = make_seq<ATTN_KEYS>(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), RT * 16);
     const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
     const int unit = local / sq.steps, t0 = local - unit * sq.steps;
     const int t1 = min(sq.steps, t0 + end - cur);
@@ -209,6 +438,9 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
     const int rows = sq.n * p.group, prefix = sq.kv - sq.n, kv = sq.kv;
     const int* table = p.page_table + (long)b * p.max_pages;
 
+    // scores in log2 units; a negative scale is taken as the queries' sign
+    const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = fabsf(scale);
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
     // queries: column i of row tile rt is row (rb RT + rt) 16 + i = (token j, head of the group)
     uint4 q[RT][Q_LDS ? 1 : G::KS];
     int jrow[RT];
@@ -219,14 +451,13 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       jrow[rt] = min(j, sq.n - 1);
       const uint16_t* src = p.q + (long)(sq.q0 + jrow[rt]) * p.ldq + (long)(h * p.group + (r - j * p.group)) * D;
       if constexpr (Q_LDS) {
-        for (int s = wave; s < G::KS; s += 4) sq_ops[s][lane] = r < rows ? ldg16(src + q_place<FP8>(s, g)) : zero4();
+        for (int s = wave; s < G::KS; s += 4) sq_ops[s][lane] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
       } else {
 #pragma unroll
-        for (int s = 0; s < G::KS; ++s) q[rt][s] = r < rows ? ldg16(src + q_place<FP8>(s, g)) : zero4();
+        for (int s = 0; s < G::KS; ++s) q[rt][s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
       }
     }
     if constexpr (Q_LDS) __syncthreads();
-    const float sc = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2;
 
     v4f o[RT][NT];
     float m[RT], l[RT];
@@ -266,19 +497,6 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
     };
 
     constexpr int VE = G::NCH * G::CH / 2;  // words of a lane's V values of one key, in bf16
-    auto widen_v = [](const uint32_t* in, uint32_t* out) {
-      if constexpr (FP8) {
-#pragma unroll
-        for (int w = 0; w < G::NCH * G::VW; ++w) {
-          const uint2 u = fp8x4_to_bf16(in[w]);
-          out[2 * w] = u.x;
-          out[2 * w + 1] = u.y;
-        }
-      } else {
-#pragma unroll
-        for (int w = 0; w < VE; ++w) out[w] = in[w];
-      }
-    };
     int key0 = t0 * ATTN_KEYS + wave * 32;
     int id0 = 0, id1 = 0, n0 = 0, n1 = 0;  // pages of this step and of the next one
     long b0 = 0, b1 = 0;
@@ -304,14 +522,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
         if constexpr (Q_LDS) qs = sq_ops[st][lane];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
-          uint4 a;
-          if constexpr (FP8) {
-            const uint4 w = kr[kt][st >> 1];
-            const uint2 lo = fp8x4_to_bf16((st & 1) ? w.z : w.x), hi = fp8x4_to_bf16((st & 1) ? w.w : w.y);
-            a = make_uint4(lo.x, lo.y, hi.x, hi.y);
-          } else {
-            a = kr[kt][st];
-          }
+          const uint4 a = k_operand<FP8>(kr[kt], st);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) s[rt][kt] = mfma_bf16_16x16x32(a, Q_LDS ? qs : q[rt][Q_LDS ? 0 : st], s[rt][kt]);
         }
@@ -321,106 +532,37 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       const int d0 = key0 + 8 * g - prefix;  // draft place of this lane's 8 keys
       const bool gone = g < 2 ? bad0 : bad1;
       uint4 pb[RT];
-      uint32_t vis[RT];
+      uint32_t vis[RT] = {};
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float x[8];  // scores of keys 8 g + e, in log2 units
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = s[rt][e >> 2][e & 3] * sc;
         if constexpr (SPECIAL) {
           const uint64_t* mrow = p.mask ? p.mask + (long)(sq.q0 + jrow[rt]) * p.words : nullptr;
           vis[rt] = gone ? 0u : visible8(mrow, p.words, jrow[rt], d0, sq.n);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = (vis[rt] >> e) & 1u ? x[e] : NEG_INF;
         }
-        float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        if (__any(mx > m[rt] + SLACK)) {
-          mx = fmaxf(mx, __shfl_xor(mx, 16));
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
-          // each row by its own scores alone: what a row gets does not depend on its neighbours
-          const bool up = mx > m[rt] + SLACK;
-          const float f = up ? __builtin_amdgcn_exp2f(m[rt] - mx) : 1.f;
-          m[rt] = up ? mx : m[rt];
-          l[rt] *= f;
-#pragma unroll
-          for (int tt = 0; tt < NT; ++tt) o[rt][tt] *= f;
-        }
-        const float ref = m[rt] == NEG_INF ? 0.f : m[rt];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __builtin_amdgcn_exp2f(x[e] - ref);
-          l[rt] += x[e];
-        }
-        // P enters the MFMA in bf16 (relative error 2^-8 an element at most, as the output's own
-        // rounding); its sum l is taken before the rounding, in 32 bits
-        pb[rt] = make_uint4(bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7]));
+        pb[rt] = softmax_step<NT, SPECIAL>(s[rt], sc, vis[rt], m[rt], l[rt], o[rt]);
       }
 
       // V: 8 keys x CH values a lane, widened to bf16
+      uint32_t odd = 0;
+      if constexpr (SPECIAL) {
+        const uint32_t mine = clean_v<FP8>(vr, g, gone, d0, sq.n);
+#pragma unroll
+        for (int gk = 0; gk < 4; ++gk) odd |= (uint32_t)__builtin_amdgcn_readlane((int)mine, 16 * gk) << (8 * gk);
+      }
       uint32_t vb[8][VE];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) widen_v(vr[e], vb[e]);
-      uint32_t odd = 0;  // keys of this lane's group with a value that is not finite
-      if constexpr (SPECIAL) {
-        // Keys past the end, and of pages that do not exist, hold anything: their rows are
-        // zeroed.  A drafted key that only some rows see must not reach the others through
-        // 0 * NaN, so rows with values that are not finite are taken out of the product and
-        // added apart, to the rows that see them.
+      for (int e = 0; e < 8; ++e) widen_v<G, FP8>(vr[e], vb[e]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool none = gone || d0 + e >= sq.n;
-          bool inf = false;
+      for (int tt = 0; tt < NT; ++tt) {
+        const uint4 a = transposed<VE>(vb, tt >> 1, tt & 1);
 #pragma unroll
-          for (int w = 0; w < VE; ++w) {
-            vb[e][w] = none ? 0u : vb[e][w];
-            inf |= ((vb[e][w] & 0x7f80u) == 0x7f80u) | ((vb[e][w] & 0x7f800000u) == 0x7f800000u);
-          }
-          const uint64_t any = __ballot(inf);
-          if ((any >> (16 * g)) & 0xffffu) {
-            odd |= 1u << e;
-#pragma unroll
-            for (int w = 0; w < VE; ++w) vb[e][w] = 0u;
-          }
-        }
+        for (int rt = 0; rt < RT; ++rt) o[rt][tt] = mfma_bf16_16x16x32(a, pb[rt], o[rt][tt]);
       }
-#pragma unroll
-      for (int c = 0; c < G::NCH; ++c)
-#pragma unroll
-        for (int e = 0; e < G::CH; ++e) {
-          const int w = c * (G::CH / 2) + (e >> 1);
-          const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
-          const uint4 a = make_uint4(__builtin_amdgcn_perm(vb[1][w], vb[0][w], sel), __builtin_amdgcn_perm(vb[3][w], vb[2][w], sel),
-                                     __builtin_amdgcn_perm(vb[5][w], vb[4][w], sel), __builtin_amdgcn_perm(vb[7][w], vb[6][w], sel));
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) o[rt][c * G::CH + e] = mfma_bf16_16x16x32(a, pb[rt], o[rt][c * G::CH + e]);
-        }
       if constexpr (SPECIAL) {
-        for (int kk = 0; kk < 32; ++kk) {
-          const int gk = kk >> 3, e = kk & 7;
-          if (!((__builtin_amdgcn_readlane((int)odd, 16 * gk) >> e) & 1)) continue;
-          // this key's row alone, as the operand whose only key it is
-          const char* row = reinterpret_cast<const char*>(p.v_cache) + (gk < 2 ? b0 : b1) + (kk & 15) * G::ROWB + i * G::VB;
-          uint32_t w1[G::NCH * G::VW], v1[VE];
+        const char* vc = reinterpret_cast<const char*>(p.v_cache);
+        if (odd)
 #pragma unroll
-          for (int c = 0; c < G::NCH; ++c) ldg_words<G::VB>(row + c * 16 * G::VB, &w1[c * G::VW]);
-          widen_v(w1, v1);
-          bool sees[RT];
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) sees[rt] = (__shfl((int)vis[rt], 16 * gk + i) >> e) & 1;
-#pragma unroll
-          for (int tt = 0; tt < NT; ++tt) {
-            const uint32_t half = (v1[tt >> 1] >> (16 * (tt & 1))) & 0xffffu;
-            const uint32_t val = g == gk ? half << (16 * (e & 1)) : 0u;
-            const uint4 a = make_uint4((e >> 1) == 0 ? val : 0u, (e >> 1) == 1 ? val : 0u, (e >> 1) == 2 ? val : 0u, (e >> 1) == 3 ? val : 0u);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const v4f add = mfma_bf16_16x16x32(a, pb[rt], v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int r = 0; r < 4; ++r) o[rt][tt][r] += sees[rt] ? add[r] : 0.f;
-            }
-            __builtin_amdgcn_sched_barrier(0);  // one tile at a time: this path is rare, its registers are not
-          }
-        }
+          for (int rt = 0; rt < RT; ++rt) add_odd_keys<D, FP8>(odd, vc + b0, vc + b1, pb[rt], vis[rt], o[rt]);
         if ((bad0 || bad1) && lane == 0 && p.status) or_agent(p.status, ST_PAGE);
         if (more) load_k(nb0, nb1);  // a unit's few last steps: its registers serve the above till here
       }
@@ -500,50 +642,435 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
-      const int last = (cur + sq.steps - 1) / per;  // workgroup that holds the unit's last step
-      *reinterpret_cast<int4*>(p.desc + 4 * wg) = make_int4(last - wg + 1, b, h, rb);
+      put_desc(p, wg, mine.pieces ? mine.pieces : (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
     }
     cur += t1 - t0;
   }
 }
 
-// Joins the pieces of a unit cut between workgroups: grid (workgroups, row groups of 4), a
-// wave a row, lanes over the values and, where they are fewer than 64 x 4, over the pieces.
-template <int D>
+// Joins the pieces of a unit cut between workgroups: grid (workgroups, row groups).  The lanes
+// of a wave go over a row's values and, where those are fewer than 64 x 4, over the pieces; the
+// four waves take a row each, or with WIDE a row's pieces in turn.
+template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int block_rows) {
   const int wg = blockIdx.x;
-  const int4 ds = *reinterpret_cast<const int4*>(p.desc + 4 * wg);
+  const int4 ds = *reinterpret_cast<const int4*>(p.desc + ATTN_DESC * wg);
+  const int rb = p.desc[ATTN_DESC * wg + 4];
   if (ds.x == 0) return;
-  constexpr int CL = D / 4, PG = 64 / CL;  // lanes over a row's values, groups of lanes over the pieces
-  const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
-  const int q0 = p.q_indptr[ds.y], rows = (p.q_indptr[ds.y + 1] - q0) * p.group;
-  const int r = ds.w * block_rows + row;
-  if (row >= block_rows || r >= rows) return;
+  constexpr int CL = D / 4;                        // lanes over a row's values
+  constexpr int PW = 64 / CL, PG = PW * (WIDE ? 4 : 1);  // groups of lanes over the pieces: a wave's, all
+  __shared__ float4 so[WIDE ? 4 : 1][CL];
+  __shared__ float2 sml[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row = WIDE ? blockIdx.y : blockIdx.y * 4 + wave;
+  const int r = rb * block_rows + row;
+  if (row >= block_rows || r >= ds.z) return;  // WIDE: the whole workgroup
   auto slot = [&](int k) { return (long)(k == 0 ? 2 * wg + 1 : 2 * (wg + k)) * block_rows + row; };
-  float M = NEG_INF;
-  for (int k = lane; k < ds.x; k += 64) M = fmaxf(M, p.part_ml[2 * slot(k)]);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-  const int c4 = lane % CL, pg = lane / CL;
-  float L = 0.f;
+  const int c4 = lane % CL, pg = lane / CL + (WIDE ? PW * wave : 0);
+  float M = NEG_INF, L = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = pg; k < ds.x; k += PG) {
-    const long at = slot(k);
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * c4);
-    const float f = ml.x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml.x - M);
-    L += ml.y * f;
-    a.x += v.x * f; a.y += v.y * f; a.z += v.z * f; a.w += v.w * f;
+  // eight pieces a round with a running maximum: all of a round's loads are in flight together
+  for (int k0 = pg; k0 < ds.x; k0 += 8 * PG) {
+    float2 ml[8];
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const long at = slot(min(k0 + k * PG, ds.x - 1));  // the last piece again, with no weight
+      ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+      v[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * c4);
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
+    const float back = M == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(M - mn);
+    L *= back; a.x *= back; a.y *= back; a.z *= back; a.w *= back;
+    M = mn;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // selected, not branched around: a branch would pull the loads apart, one wait each
+      const bool real = k0 + k * PG < ds.x;
+      const float f = ml[k].x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[k].x - M);
+      L += real ? ml[k].y * f : 0.f;
+      a.x += real ? v[k].x * f : 0.f; a.y += real ? v[k].y * f : 0.f; a.z += real ? v[k].z * f : 0.f; a.w += real ? v[k].w * f : 0.f;
+    }
+  }
+  {  // the groups of lanes hold other pieces of the same row
+    float mn = M;
+#pragma unroll
+    for (int d = CL; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d));
+    const float f = M == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(M - mn);
+    L *= f; a.x *= f; a.y *= f; a.z *= f; a.w *= f;
+    M = mn;
   }
 #pragma unroll
   for (int d = CL; d < 64; d <<= 1) {
     L += __shfl_xor(L, d);
     a.x += __shfl_xor(a.x, d); a.y += __shfl_xor(a.y, d); a.z += __shfl_xor(a.z, d); a.w += __shfl_xor(a.w, d);
   }
-  if (pg) return;
-  const float vs = p.v_scale ? p.v_scale[ds.z] : 1.f;
-  put_row<D>(p, q0, ds.z, r, c4, a, M, L, vs);
+  if constexpr (WIDE) {
+    if (lane < CL) so[wave][c4] = a;
+    if (lane == 0) sml[wave] = make_float2(M, L);
+    __syncthreads();
+    if (wave) return;
+    M = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
+    L = 0.f;
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = sml[w].x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(sml[w].x - M);
+      const float4 v = so[w][c4];
+      L += sml[w].y * f;
+      a.x += v.x * f; a.y += v.y * f; a.z += v.z * f; a.w += v.w * f;
+    }
+  }
+  if (lane >= CL) return;
+  put_row<D>(p, ds.y, ds.w, r, c4, a, M, L, p.v_scale ? p.v_scale[ds.w] : 1.f);
+}
+
+template <typename T>
+__device__ __forceinline__ void swap_regs(T& a, T& b) {
+  const T t = a;
+  a = b;
+  b = t;
+}
+template <typename T, int N>
+__device__ __forceinline__ void swap_regs(T (&a)[N], T (&b)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) swap_regs(a[k], b[k]);
+}
+
+// The same for many rows (trees of many tokens times a group of heads; a prompt's chunk): eight
+// waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128 RT rows, put into LDS as
+// MFMA operands (K and the transposed V in bf16, 1 KB a wave's read, conflict free; an 8-bit
+// cache is widened once, here), and each wave takes 16 RT rows through all of them, so nothing
+// is joined inside the workgroup.  The next step's loads are in flight, in registers, while a
+// step is computed.  Tiles of 16 rows are dealt to the waves in turn.
+// A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
+// of O^T, so that its stores and the join's loads are whole KBs and a wave of the join, which
+// takes one x, has neighbouring values of a row.
+constexpr int ROW_WAVES = 8;
+
+template <int D, int RT, bool FP8>
+__global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeAttnParams p) {
+  using G = Geo<D, FP8>;
+  constexpr int NT = D / 16, BLOCK = 16 * RT * ROW_WAVES;
+  constexpr int KEYS = RT == 1 ? ATTN_KEYS : ATTN_SHARED_KEYS;  // of a step: the finer, the more even the pieces
+  constexpr int VE = G::NCH * G::CH / 2;
+  __shared__ uint4 sk[4][2][G::KS][64];  // [32 keys][16 keys][MFMA step][lane]
+  __shared__ uint4 sv[4][NT][64];        // [32 keys][tile of O^T][lane]
+  __shared__ uint32_t s_odd[4], s_bad[4];
+  __shared__ int wave_sum[ROW_WAVES];
+  __shared__ Stretch found;
+  extern __shared__ int cum[];
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave >> 1;          // the 32 keys of a step this wave loads
+  const bool loads_v = wave & 1;      // their values, or their keys
+  const int wg = (blockIdx.x & 7) * (p.n_wg >> 3) + (blockIdx.x >> 3);
+
+  const Stretch mine = find_stretch<64 * ROW_WAVES, KEYS, RT == 2>(p, wg, BLOCK, cum, wave_sum, &found);
+  if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
+  int cur = mine.cur, b = mine.b;
+  const int end = mine.end;
+
+  const int page = 1 << p.page_log2;
+  // this lane's first byte of a half of 16 keys, and which half it loads
+  const int off = loads_v ? 8 * (g & 1) * G::ROWB + i * G::VB : (8 * ((i >> 2) & 1) + (i & 3)) * G::ROWB + 16 * g;
+  const bool second = loads_v ? g >= 2 : i >= 8;
+
+  while (cur < end) {
+    while (cum[b + 1] <= cur) ++b;
+    b = __builtin_amdgcn_readfirstlane(b);
+    const Seq sq = make_seq<KEYS>(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), BLOCK);
+    const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
+    const int unit = local / sq.steps, t0 = local - unit * sq.steps;
+    const int t1 = min(sq.steps, t0 + end - cur);
+    const int h = unit / sq.blocks, rb = unit - h * sq.blocks;
+    constexpr int PER_STEP = KEYS / ATTN_GROUP;
+    const int g0 = t0 * PER_STEP, g1 = t1 * PER_STEP;  // in groups of 32 keys
+    const int rows = sq.n * p.group, prefix = sq.kv - sq.n;
+    // without a mask no row of this block sees past its last token
+    const int last_row = min(rows, (rb + 1) * BLOCK) - 1;
+    const int kv = p.mask ? sq.kv : min(sq.kv, prefix + last_row / p.group + 1);
+    const int* table = p.page_table + (long)b * p.max_pages;
+
+    // this wave's loads of a step: V [8 keys][words], or K [16 keys][load] in the same words
+    constexpr int SW = G::NCH * G::VW;
+    static_assert(2 * G::KL * 4 == 8 * SW, "keys and values take the same registers");
+    uint32_t st[8][SW];
+    auto kw = [&](int kt, int c, int x) -> uint32_t& { return st[(4 * (kt * G::KL + c) + x) / SW][(4 * (kt * G::KL + c) + x) % SW]; };
+    int id0 = 0, id1 = 0;
+    auto fetch = [&](int t) {  // a round: up to four groups from t on
+      const int key = (t + grp) * ATTN_GROUP;
+      if (t + grp >= g1 || key >= kv) return;
+      const int last = (sq.kv - 1) >> p.page_log2;
+      id0 = ld_table(table + min(key >> p.page_log2, last));
+      id1 = ld_table(table + min((key + 16) >> p.page_log2, last));
+      auto base = [&](int id, int k) {
+        const int ok = (unsigned)id < (unsigned)p.n_pages ? id : 0;
+        return ((((long)ok * p.n_kv + h) << p.page_log2) + (k & (page - 1))) * G::ROWB;
+      };
+      const long b0 = base(id0, key), b1 = base(id1, key + 16);
+      if (loads_v) {
+        const char* src = reinterpret_cast<const char*>(p.v_cache) + (second ? b1 : b0) + off;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int c = 0; c < G::NCH; ++c) ldg_words<G::VB>(src + e * G::ROWB + c * 16 * G::VB, &st[e][c * G::VW]);
+      } else {
+        const char* src = reinterpret_cast<const char*>(p.k_cache) + (second ? b1 : b0) + off;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int c = 0; c < G::KL; ++c) {
+            const uint4 w = ldg16(src + kt * 4 * G::ROWB + 64 * c);
+            kw(kt, c, 0) = w.x; kw(kt, c, 1) = w.y; kw(kt, c, 2) = w.z; kw(kt, c, 3) = w.w;
+          }
+      }
+    };
+    auto stage = [&](int t) {
+      const int key = (t + grp) * ATTN_GROUP;
+      if (t + grp >= g1 || key >= kv) return;
+      const bool bad0 = (unsigned)id0 >= (unsigned)p.n_pages, bad1 = (unsigned)id1 >= (unsigned)p.n_pages;
+      if (loads_v) {
+        uint32_t odd = 0;
+        if (key + 32 > prefix || bad0 || bad1) {
+          const uint32_t mine = clean_v<FP8>(st, g, g < 2 ? bad0 : bad1, key + 8 * g - prefix, sq.n);
+#pragma unroll
+          for (int gk = 0; gk < 4; ++gk) odd |= (uint32_t)__builtin_amdgcn_readlane((int)mine, 16 * gk) << (8 * gk);
+        }
+        if (lane == 0) s_odd[grp] = odd;
+        if constexpr (FP8) {  // a word of the eight rows at a time: four tiles
+#pragma unroll
+          for (int w = 0; w < SW; ++w) {
+            uint32_t vb[8][2];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint2 u = fp8x4_to_bf16(st[e][w]);
+              vb[e][0] = u.x;
+              vb[e][1] = u.y;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sv[grp][4 * w + x][lane] = transposed<2>(vb, x >> 1, x & 1);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        } else {
+#pragma unroll
+          for (int tt = 0; tt < NT; ++tt) sv[grp][tt][lane] = transposed<VE>(st, tt >> 1, tt & 1);
+        }
+      } else {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          uint4 kr[G::KL];
+#pragma unroll
+          for (int c = 0; c < G::KL; ++c) kr[c] = make_uint4(kw(kt, c, 0), kw(kt, c, 1), kw(kt, c, 2), kw(kt, c, 3));
+#pragma unroll
+          for (int s = 0; s < G::KS; ++s) sk[grp][kt][s][lane] = k_operand<FP8>(kr, s);
+        }
+        if (lane == 0) {
+          s_bad[grp] = (bad0 ? 1u : 0u) | (bad1 ? 2u : 0u);
+          if ((bad0 || bad1) && p.status) or_agent(p.status, ST_PAGE);
+        }
+      }
+    };
+    fetch(g0);
+
+    // scores in log2 units; a negative scale is taken as the queries' sign
+    const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = fabsf(scale);
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+    // queries: row tile rt ROW_WAVES + wave of the block, column i
+    uint4 q[RT][G::KS];
+    int tiles = 0;  // of this wave that hold rows
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = rb * BLOCK + (rt * ROW_WAVES + wave) * 16 + i;
+      if (r - i < rows) tiles = rt + 1;
+      const int j = r / p.group;
+      const uint16_t* src = p.q + (long)(sq.q0 + min(j, sq.n - 1)) * p.ldq + (long)(h * p.group + (r - j * p.group)) * D;
+#pragma unroll
+      for (int s = 0; s < G::KS; ++s) q[rt][s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
+    }
+    v4f o[RT][NT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      m[rt] = NEG_INF;
+      l[rt] = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[rt][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // 32 keys for the first COUNT of the wave's row tiles; SPECIAL: for the tile in the first's
+    // place, which is tile rt0
+    auto group = [&](auto special_t, auto count_t, int gr, int key0, uint32_t bad, int rt0) {
+      constexpr bool SPECIAL = decltype(special_t)::value;
+      constexpr int COUNT = decltype(count_t)::value;
+      v4f s[COUNT][2];
+#pragma unroll
+      for (int rt = 0; rt < COUNT; ++rt) s[rt][0] = s[rt][1] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < G::KS; ++x)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const uint4 a = sk[gr][kt][x][lane];
+#pragma unroll
+          for (int rt = 0; rt < COUNT; ++rt) s[rt][kt] = mfma_bf16_16x16x32(a, q[rt][x], s[rt][kt]);
+          if (D == 256 && kt == 1) __builtin_amdgcn_sched_barrier(0);  // operands in pairs: all at once spill
+        }
+      uint4 pb[COUNT];
+      uint32_t vis[COUNT] = {};
+#pragma unroll
+      for (int rt = 0; rt < COUNT; ++rt) {
+        if constexpr (SPECIAL) {
+          const int j = min((rb * BLOCK + (rt0 * ROW_WAVES + wave) * 16 + i) / p.group, sq.n - 1);
+          const uint64_t* mrow = p.mask ? p.mask + (long)(sq.q0 + j) * p.words : nullptr;
+          vis[rt] = (bad >> (g >> 1)) & 1u ? 0u : visible8(mrow, p.words, j, key0 + 8 * g - prefix, sq.n);
+        }
+        pb[rt] = softmax_step<NT, SPECIAL>(s[rt], sc, vis[rt], m[rt], l[rt], o[rt]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) {
+        const uint4 a = sv[gr][tt][lane];
+#pragma unroll
+        for (int rt = 0; rt < COUNT; ++rt) o[rt][tt] = mfma_bf16_16x16x32(a, pb[rt], o[rt][tt]);
+        if (D == 256 && (tt & 1)) __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (SPECIAL) {
+        static_assert(COUNT == 1, "one row tile at a time");
+        const uint32_t odd = __builtin_amdgcn_readfirstlane((int)s_odd[gr]);
+        if (odd) {
+          auto at = [&](int key) {
+            const int id = ld_table(table + (key >> p.page_log2));  // a page that exists: its keys are seen
+            return reinterpret_cast<const char*>(p.v_cache) + ((((long)id * p.n_kv + h) << p.page_log2) + (key & (page - 1))) * G::ROWB;
+          };
+          add_odd_keys<D, FP8>(odd, odd & 0xffffu ? at(key0) : nullptr, odd >> 16 ? at(key0 + 16) : nullptr, pb[0], vis[0], o[0]);
+        }
+      }
+    };
+    using std::integral_constant;
+
+    for (int t = g0; t < g1; t += 4) {
+      __syncthreads();  // the round before is read
+      stage(t);
+      if (t + 4 < g1) fetch(t + 4);
+      __syncthreads();
+      for (int gr = 0; gr < 4 && t + gr < g1; ++gr) {
+        const int key0 = (t + gr) * ATTN_GROUP;
+        if (key0 >= kv || tiles == 0) break;
+        const uint32_t bad = __builtin_amdgcn_readfirstlane((int)s_bad[gr]);
+        if (key0 + 32 > prefix || bad) {
+          // one row tile at a time, each in the first's registers: these few groups' code for
+          // two would spill
+          for (int rt0 = 0; rt0 < tiles; ++rt0) {
+            group(std::true_type{}, integral_constant<int, 1>{}, gr, key0, bad, rt0);
+            if constexpr (RT == 2) {
+              if (tiles == 2) {
+                swap_regs(q[0], q[1]);
+                swap_regs(o[0], o[1]);
+                swap_regs(m[0], m[1]);
+                swap_regs(l[0], l[1]);
+              }
+            }
+          }
+        } else if (tiles == RT) {
+          group(std::false_type{}, integral_constant<int, RT>{}, gr, key0, 0, 0);
+        } else {
+          group(std::false_type{}, integral_constant<int, 1>{}, gr, key0, 0, 0);
+        }
+      }
+    }
+
+    const bool whole = t0 == 0 && t1 == sq.steps;
+    const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
+    const float vs = FP8 ? p.v_scale[h] : 1.f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (rt >= tiles) break;
+      const int tile = rt * ROW_WAVES + wave, r = rb * BLOCK + tile * 16 + i;
+      l[rt] += __shfl_xor(l[rt], 16);
+      l[rt] += __shfl_xor(l[rt], 32);
+      if (whole) {
+        put_tile<D, G::CH>(p, sq.q0, rows, h, r, g, o[rt], m[rt], l[rt], vs);
+      } else {
+        float* dst = p.part_o + ((long)slot * (BLOCK / 16) + tile) * (16 * D) + 4 * lane;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int t4 = 0; t4 < NT; t4 += 4)
+            *reinterpret_cast<float4*>(dst + (x * (NT / 4) + t4 / 4) * 256) =
+                make_float4(o[rt][t4][x], o[rt][t4 + 1][x], o[rt][t4 + 2][x], o[rt][t4 + 3][x]);
+        if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + tile * 16 + i)) = make_float2(m[rt], l[rt]);
+      }
+    }
+    if (!whole && t0 == 0 && tid == 0) {
+      put_desc(p, wg, mine.pieces ? mine.pieces : (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
+    }
+    cur += t1 - t0;
+  }
+}
+
+// Joins the pieces of k_tree_attention_rows: a workgroup a row tile, a wave one x of it.  The
+// pieces are taken four at a time with a running maximum, so that all loads of a round, the
+// pieces' (m, l) among them, are in flight together: the launch is a chain of latencies (a
+// pass of its own over the maxima, and a wave for a whole tile, took 10.8 us at 64 rows).
+template <int D, int CH>
+__global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int block_rows) {
+  constexpr int NV = D / 64;  // float4 of a lane
+  const int wg = blockIdx.x, tile = blockIdx.y;
+  const int4 ds = *reinterpret_cast<const int4*>(p.desc + ATTN_DESC * wg);
+  const int rb = p.desc[ATTN_DESC * wg + 4];
+  if (ds.x == 0) return;
+  const int lane = threadIdx.x & 63, x = threadIdx.x >> 6, g = lane >> 4;
+  const int rows = ds.z, r = rb * block_rows + tile * 16 + (lane & 15);
+  if (r - (lane & 15) >= rows) return;
+  const float* ml = p.part_ml + 2 * (tile * 16 + (lane & 15));
+  const float* src = p.part_o + (long)tile * (16 * D) + x * NV * 256 + 4 * lane;
+  float M = NEG_INF, L = 0.f;
+  float4 o[NV];
+#pragma unroll
+  for (int t = 0; t < NV; ++t) o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < ds.x; k0 += 4) {
+    float2 v[4];
+    float4 u[4][NV];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int kk = min(k0 + k, ds.x - 1);  // the last piece again, with no weight
+      const long slot = kk == 0 ? 2 * wg + 1 : 2 * (wg + kk);
+      v[k] = *reinterpret_cast<const float2*>(ml + 2 * slot * block_rows);
+#pragma unroll
+      for (int t = 0; t < NV; ++t) u[k][t] = *reinterpret_cast<const float4*>(src + slot * block_rows * D + t * 256);
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, v[k].x);
+    const float back = M == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(M - mn);
+    L *= back;
+#pragma unroll
+    for (int t = 0; t < NV; ++t) { o[t].x *= back; o[t].y *= back; o[t].z *= back; o[t].w *= back; }
+    M = mn;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // selected, not branched around: a branch would pull the loads apart, one wait each
+      const bool real = k0 + k < ds.x;
+      const float f = v[k].x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(v[k].x - M);
+      L += real ? v[k].y * f : 0.f;
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        o[t].x += real ? u[k][t].x * f : 0.f; o[t].y += real ? u[k][t].y * f : 0.f;
+        o[t].z += real ? u[k][t].z * f : 0.f; o[t].w += real ? u[k][t].w * f : 0.f;
+      }
+    }
+  }
+  if (r >= rows) return;
+  const float inv = L == 0.f ? 0.f : (p.v_scale ? p.v_scale[ds.w] : 1.f) / L;
+  const int j = r / p.group;
+  const long at = (long)(ds.y + j) * p.n_q + ds.w * p.group + (r - j * p.group);
+#pragma unroll
+  for (int t = 0; t < NV; ++t)  // tiles 4 t .. 4 t + 3: chunk 4 t / CH, places e = 4 t % CH ..
+    *reinterpret_cast<uint2*>(p.out + at * D + 16 * CH * (4 * t / CH) + CH * (4 * g + x) + 4 * t % CH) =
+        make_uint2(bf16x2_rne(o[t].x * inv, o[t].y * inv), bf16x2_rne(o[t].z * inv, o[t].w * inv));
+  if (g == 0 && x == 0 && p.lse) p.lse[at] = L == 0.f ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
 }
 
 // Bit i of row t: drafted token i is t or one of its ancestors.  One thread a token; a parent
@@ -577,33 +1104,59 @@ __global__ __launch_bounds__(256) void k_tree_mask(const int* parents, const int
 }
 
 template <int D, int RT, bool FP8>
-void launch_one(const TreeAttnParams& p, hipStream_t s) {
+void launch_few(const TreeAttnParams& p, hipStream_t s) {
   constexpr int OCC = RT == 1 && D <= 128 ? 2 : 1;
   hipLaunchKernelGGL((k_tree_attention<D, RT, FP8, OCC>), dim3(p.n_wg), dim3(256), (p.B + 1) * sizeof(int), s, p);
+  const int rows = min(RT * 16, p.max_q * p.group);
+  // a workgroup a row where few units are cut into many pieces (64 pieces of 4 rows: 5.9 us
+  // against 9.0; 4 pieces of 4 rows 5.6 against 4.0)
+  if (rows <= 4 && p.B * p.n_kv * 16 <= p.n_wg)
+    hipLaunchKernelGGL((k_tree_combine<D, true>), dim3(p.n_wg, rows), dim3(256), 0, s, p, RT * 16);
+  else
+    hipLaunchKernelGGL((k_tree_combine<D, false>), dim3(p.n_wg, (rows + 3) / 4), dim3(256), 0, s, p, RT * 16);
 }
 
-template <int D>
-hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, bool fp8, hipStream_t s) {
-  switch (pl.row_tiles) {
-    case 1: fp8 ? launch_one<D, 1, true>(p, s) : launch_one<D, 1, false>(p, s); break;
-    default:
-      if constexpr (D <= 128) fp8 ? launch_one<D, 2, true>(p, s) : launch_one<D, 2, false>(p, s);
+template <int D, int RT, bool FP8>
+void launch_rows(const TreeAttnParams& p, hipStream_t s) {
+  constexpr int BLOCK = 16 * RT * ROW_WAVES;
+  hipLaunchKernelGGL((k_tree_attention_rows<D, RT, FP8>), dim3(p.n_wg), dim3(64 * ROW_WAVES), (p.B + 1) * sizeof(int), s, p);
+  const long rows = min((long)BLOCK, (long)p.max_q * p.group);
+  hipLaunchKernelGGL((k_tree_combine_rows<D, Geo<D, FP8>::CH>), dim3(p.n_wg, (unsigned)((rows + 15) / 16)), dim3(256), 0, s, p, BLOCK);
+}
+
+template <int D, bool FP8>
+hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t s) {
+  if (pl.shared) {
+    if constexpr (D <= 128) {
+      if (pl.row_tiles == 1) launch_rows<D, 1, FP8>(p, s);
+      else launch_rows<D, 2, FP8>(p, s);
+    } else if constexpr (FP8) {
+      launch_rows<D, 1, FP8>(p, s);
+    }
+  } else {
+    if (pl.row_tiles == 1) launch_few<D, 1, FP8>(p, s);
+    else if constexpr (D <= 128) launch_few<D, 2, FP8>(p, s);
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int rows = min(pl.row_tiles * 16, p.max_q * p.group);
-  hipLaunchKernelGGL(k_tree_combine<D>, dim3(p.n_wg, (rows + 3) / 4), dim3(256), 0, s, p, pl.row_tiles * 16);
   return hipGetLastError();
 }
 
 }  // namespace
 
-TreeAttnPlan tree_attn_plan(int D, int rows) {
+TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   TreeAttnPlan pl;
-  pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;
-  pl.n_wg = pl.row_tiles == 1 && D <= 128 ? 512 : 256;
-  const size_t slots = 2 * (size_t)pl.n_wg, r = (size_t)pl.row_tiles * 16;
-  pl.desc_bytes = (size_t)pl.n_wg * 16;
+  // 16-bit heads of 256 do not fit the registers of a wave that also holds a step's loads
+  pl.shared = rows > (D > 128 ? 16 : 32) && (D <= 128 || fp8);
+  if (pl.shared) {
+    pl.row_tiles = rows <= 16 * ROW_WAVES || D > 128 ? 1 : 2;
+    pl.block_rows = 16 * ROW_WAVES * pl.row_tiles;
+    pl.n_wg = 256;
+  } else {
+    pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;
+    pl.block_rows = 16 * pl.row_tiles;
+    pl.n_wg = pl.row_tiles == 1 && D <= 128 ? 512 : 256;
+  }
+  const size_t slots = 2 * (size_t)pl.n_wg, r = (size_t)pl.block_rows;
+  pl.desc_bytes = (size_t)pl.n_wg * ATTN_DESC * 4;
   pl.ml_bytes = slots * r * 8;
   pl.o_bytes = slots * r * D * 4;
   return pl;
@@ -611,9 +1164,9 @@ TreeAttnPlan tree_attn_plan(int D, int rows) {
 
 hipError_t launch_tree_attention(const TreeAttnParams& p, const TreeAttnPlan& pl, int D, bool fp8, hipStream_t s) {
   switch (D) {
-    case 64: return launch_d<64>(p, pl, fp8, s);
-    case 128: return launch_d<128>(p, pl, fp8, s);
-    default: return launch_d<256>(p, pl, fp8, s);
+    case 64: return fp8 ? launch_d<64, true>(p, pl, s) : launch_d<64, false>(p, pl, s);
+    case 128: return fp8 ? launch_d<128, true>(p, pl, s) : launch_d<128, false>(p, pl, s);
+    default: return fp8 ? launch_d<256, true>(p, pl, s) : launch_d<256, false>(p, pl, s);
   }
 }
 
