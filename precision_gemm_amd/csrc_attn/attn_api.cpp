@@ -63,8 +63,6 @@ inline size_t plan_bytes(const TreeAttnPlan& pl) {
   return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
 }
 
-inline int bwd_wgs(int32_t T) { return T < 4 * ROPE_BWD_WGS ? (T + 3) / 4 : ROPE_BWD_WGS; }
-
 }  // namespace
 
 extern "C" {
@@ -116,7 +114,7 @@ lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* 
 
 size_t lora_qk_norm_rope_backward_workspace_bytes(int32_t T, int32_t D) {
   if (T < 1 || T > MAX_TOKENS || (D != 64 && D != 128 && D != 256)) return 0;
-  return (size_t)bwd_wgs(T) * 2 * D * sizeof(float);
+  return (size_t)ROPE_BWD_WGS * D * sizeof(float);
 }
 
 lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, const uint16_t* dq,
@@ -145,7 +143,6 @@ lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const in
   p.cos_sin = cos_sin; p.max_pos = max_pos; p.rot = rot; p.interleaved = interleaved; p.eps = eps;
   p.dq = dq; p.dk = dk; p.dv = dv; p.dqkv = dqkv; p.ldd = ldd;
   p.part = reinterpret_cast<float*>(workspace); p.status = status;
-  p.n_wg = bwd_wgs(T);
   return launch_norm_rope_bwd(p, D, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -202,7 +199,7 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   const TreeAttnPlan pl = tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows, fp8);
   // all steps of a call are numbered in 32 bits
   const double steps = (double)B * n_kv * (double)((rows + pl.block_rows - 1) / pl.block_rows) *
-                       ((double)max_pages * page_size / (pl.shared ? ATTN_SHARED_KEYS : ATTN_KEYS) + 1.0);
+                       ((double)max_pages * page_size / ATTN_KEYS + 1.0);
   if (steps > 2.0e9) return LORA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < plan_bytes(pl))
     return LORA_ERR_WORKSPACE;

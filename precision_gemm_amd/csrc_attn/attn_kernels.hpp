@@ -45,14 +45,14 @@ struct RopeBwdParams {
   const uint16_t *dq, *dk, *dv;      // dense rows; dv may be null
   uint16_t* dqkv;
   long ldd;
-  float* part;                       // [n_wg][2][D]
+  float* part;                       // [n_wg][D]
   float *dqw, *dkw;
   int* status;
-  int rounds_q, rounds_k, rounds_v;
-  int n_wg;
+  int rounds_q, rounds_k;            // rounds of a wave over a token's query heads, key heads
+  int q_wg, n_wg;                    // workgroups of the query heads, of all
 };
 
-constexpr int ROPE_BWD_WGS = 1024;   // most workgroups of the backward, and rows of its partial sums
+constexpr int ROPE_BWD_WGS = 768;    // most workgroups of the backward (three a CU) and rows of its partial sums
 
 hipError_t launch_norm_rope(const RopeParams& p, int D, hipStream_t s);
 hipError_t launch_rope_append(const RopeParams& p, int D, bool fp8, hipStream_t s);
@@ -83,8 +83,7 @@ struct TreeAttnParams {
 constexpr int ATTN_MAX_B = 4096;     // sequences of one call (their prefix sums live in LDS)
 constexpr int ATTN_DESC = 8;         // words of a cut unit's description
 constexpr int ATTN_GROUP = 32;       // keys of one MFMA group
-constexpr int ATTN_SHARED_KEYS = 64; // keys of a step of two row tiles a wave
-constexpr int ATTN_KEYS = 128;       // keys of a workgroup step where waves split them: a group for each of four
+constexpr int ATTN_KEYS = 128;       // keys of a step: a group for each of four waves, or a round of four groups
 
 // How a call's rows (drafted tokens times query heads of a kv head) are taken: by waves that
 // split a step's keys, or (`shared`) that share them; row tiles of 16 a wave holds, rows of a

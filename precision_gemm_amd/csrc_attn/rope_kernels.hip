@@ -13,6 +13,8 @@
 // laid out and however much of the head is rotated; only the norm's sums cross lanes
 // (log2(D / 16) butterfly steps).  The 64 / (D / 16) heads of a wave's round are neighbours,
 // so its loads and stores run over whole cache lines.
+#include <algorithm>
+
 #include "attn_kernels.hpp"
 #include "../csrc/device_common.hpp"
 
@@ -201,135 +203,166 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
   }
 }
 
-// Backward.  Waves stride over the tokens; a lane meets the same 16 places of the head in
-// every round, so the weights' gradients grow in its registers and are joined at the end:
-// over the wave's slots and the workgroup's waves in LDS, in a fixed order, into one row of
-// partial sums a workgroup, which k_weight_grad adds in order (no atomics: the result does
-// not depend on timing).
+// Backward.  A workgroup takes query heads (the first q_wg workgroups) or key and value heads,
+// so that a lane, which meets the same 16 places of the head in every round, needs one set of
+// sums for the weights' gradient; a wave takes an equal, contiguous share of the (token, round)
+// pairs of its kind, the next round's loads in flight while one is computed.  The sums are
+// joined over the wave's slots and the workgroup's waves in LDS, in a fixed order, into one row
+// a workgroup, which k_weight_grad adds in order (no atomics: the result does not depend on
+// timing).
 template <int D>
-__global__ __launch_bounds__(256) void k_norm_rope_bwd(RopeBwdParams p) {
+__global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH, ROWS = 4 * SLOTS;
-  __shared__ __attribute__((aligned(16))) float red[ROWS][2 * D];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __attribute__((aligned(16))) float red[ROWS][D];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int sl = lane / LPH, j = lane % LPH;
   const LaneMap m = lane_map(j, p.rot, p.interleaved);
-  const int rounds = p.rounds_q + p.rounds_k + p.rounds_v;
-  float accq[16], acck[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) accq[e] = acck[e] = 0.f;
+  const bool kv = (int)blockIdx.x >= p.q_wg;
+  const int rounds = kv ? 2 * p.rounds_k : p.rounds_q;  // values' rounds too, without dv empty
+  const float* w = kv ? p.k_weight : p.q_weight;
+  const int n_waves = 4 * (kv ? p.n_wg - p.q_wg : p.q_wg), at = 4 * ((int)blockIdx.x - (kv ? p.q_wg : 0)) + wave;
+  const int all = p.T * rounds;
+  const int first = (int)((long)all * at / n_waves), last = (int)((long)all * (at + 1) / n_waves);
 
-  for (int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + wave)); t < p.T; t += p.n_wg * 4) {
-    int pos = p.rot ? p.positions[t] : 0;
-    const bool placed = p.rot == 0 || (unsigned)pos < (unsigned)p.max_pos;
-    if (!placed) {
-      pos = 0;
-      if (p.status && lane == 0) or_agent(p.status, ST_POSITION);
+  // a (token, round): heads h of this lane's slot, places of its gradient, input and result
+  struct Round { uint4 ga, gb, xa, xb; };
+  auto head = [&](int r, bool& value, bool& live) {
+    value = kv && r >= p.rounds_k;
+    const int h = (value ? r - p.rounds_k : r) * SLOTS + sl;
+    live = h < (kv ? p.n_kv : p.n_q) && !(value && !p.dv);
+    return h;
+  };
+  auto load = [&](int t, int r) {
+    bool value, live;
+    const int h = head(r, value, live);
+    const uint16_t* g = (kv ? (value ? p.dv : p.dk) + ((long)t * p.n_kv + h) * D : p.dq + ((long)t * p.n_q + h) * D);
+    const uint16_t* x = p.qkv + (long)t * p.ld + (long)(h + (kv ? p.n_q : 0)) * D;
+    Round v{zero4(), zero4(), zero4(), zero4()};
+    if (live) {
+      v.ga = ldg16(g + m.a);
+      v.gb = ldg16(g + m.b);
+      if (w && !value) {
+        v.xa = ldg16(x + m.a);
+        v.xb = ldg16(x + m.b);
+      }
     }
-    const Turn tn = load_turn(p.cos_sin, pos, p.rot, m);
-    for (int r = 0; r < rounds; ++r) {
-      const int kind = r < p.rounds_q ? 0 : r < p.rounds_q + p.rounds_k ? 1 : 2;
-      const int h = (r - (kind == 0 ? 0 : kind == 1 ? p.rounds_q : p.rounds_q + p.rounds_k)) * SLOTS + sl;
-      const bool live = h < (kind == 0 ? p.n_q : p.n_kv);
-      const long col = (long)(h + (kind == 0 ? 0 : kind == 1 ? p.n_q : p.n_q + p.n_kv)) * D;
-      const uint16_t* gsrc = kind == 0 ? p.dq + ((long)t * p.n_q + h) * D
-                                       : (kind == 1 ? p.dk : p.dv) + ((long)t * p.n_kv + h) * D;
-      uint16_t* dst = p.dqkv + (long)t * p.ldd + col;
-      uint4 ga = zero4(), gb = zero4(), xa = zero4(), xb = zero4();
+    return v;
+  };
+
+  float acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  int t = first / rounds, r = first - t * rounds;
+  Round next{};
+  if (first < last) next = load(t, r);
+  bool placed = true, fresh = true;
+  Turn tn;
+  for (int it = first; it < last; ++it) {
+    const Round now = next;
+    const int t0 = t, r0 = r;
+    if (fresh) {  // a token's first round here
+      int pos = p.rot ? p.positions[t0] : 0;
+      placed = p.rot == 0 || (unsigned)pos < (unsigned)p.max_pos;
+      if (!placed) {
+        pos = 0;
+        if (p.status && lane == 0) or_agent(p.status, ST_POSITION);
+      }
+      tn = load_turn(p.cos_sin, pos, p.rot, m);
+    }
+    fresh = ++r == rounds;
+    if (fresh) {
+      r = 0;
+      ++t;
+    }
+    if (it + 1 < last) next = load(t, r);
+
+    bool value, live;
+    const int h = head(r0, value, live);
+    uint16_t* dst = p.dqkv + (long)t0 * p.ldd + (long)(h + (kv ? (value ? p.n_q + p.n_kv : p.n_q) : 0)) * D;
+    if (value) {  // values pass through
       if (live) {
-        ga = ldg16(gsrc + m.a);
-        gb = ldg16(gsrc + m.b);
+        *reinterpret_cast<uint4*>(dst + m.a) = now.ga;
+        *reinterpret_cast<uint4*>(dst + m.b) = now.gb;
       }
-      if (kind == 2) {  // values pass through
-        if (live) {
-          *reinterpret_cast<uint4*>(dst + m.a) = ga;
-          *reinterpret_cast<uint4*>(dst + m.b) = gb;
+      continue;
+    }
+    float g[16];
+    widen(now.ga, g);
+    widen(now.gb, g + 8);
+    turn<-1>(g, tn, p.interleaved, m.turns);
+    if (w) {
+      float x[16];
+      widen(now.xa, x);
+      widen(now.xb, x + 8);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss += x[e] * x[e];
+      const float rs = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / D) + p.eps);
+      float dot = 0.f;
+      const bool count = live && placed;
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
+        const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * q4 + i;
+          x[e] *= rs;                       // xh
+          acc[e] += count ? g[e] * x[e] : 0.f;
+          g[e] *= ww[i];
+          dot += g[e] * x[e];
         }
-        continue;
       }
-      const float* w = kind == 0 ? p.q_weight : p.k_weight;
-      if (live && w) {
-        const uint16_t* src = p.qkv + (long)t * p.ld + col;
-        xa = ldg16(src + m.a);
-        xb = ldg16(src + m.b);
-      }
-      float g[16];
-      widen(ga, g);
-      widen(gb, g + 8);
-      turn<-1>(g, tn, p.interleaved, m.turns);
-      if (w) {
-        float x[16];
-        widen(xa, x);
-        widen(xb, x + 8);
-        float ss = 0.f;
+      const float mean = head_sum<LPH>(dot) * (1.0f / D);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss += x[e] * x[e];
-        const float rs = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / D) + p.eps);
-        float dot = 0.f;
-        const bool count = live && placed;
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
-          const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 4 * q4 + i;
-            x[e] *= rs;                       // xh
-            const float d = count ? g[e] * x[e] : 0.f;
-            if (kind == 0) accq[e] += d; else acck[e] += d;
-            g[e] *= ww[i];
-            dot += g[e] * x[e];
-          }
-        }
-        const float mean = head_sum<LPH>(dot) * (1.0f / D);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = rs * (g[e] - x[e] * mean);
-      }
-      if (live) {
-        *reinterpret_cast<uint4*>(dst + m.a) = placed ? narrow(g) : zero4();
-        *reinterpret_cast<uint4*>(dst + m.b) = placed ? narrow(g + 8) : zero4();
-      }
+      for (int e = 0; e < 16; ++e) g[e] = rs * (g[e] - x[e] * mean);
+    }
+    if (live) {
+      *reinterpret_cast<uint4*>(dst + m.a) = placed ? narrow(g) : zero4();
+      *reinterpret_cast<uint4*>(dst + m.b) = placed ? narrow(g + 8) : zero4();
     }
   }
-  if (!p.q_weight) return;
+  if (!w) return;
   float* row = red[wave * SLOTS + sl];
 #pragma unroll
-  for (int q4 = 0; q4 < 4; ++q4) {
-    const int o = (q4 < 2 ? m.a : m.b - 8) + 4 * q4;
-    *reinterpret_cast<float4*>(row + o) = make_float4(accq[4 * q4], accq[4 * q4 + 1], accq[4 * q4 + 2], accq[4 * q4 + 3]);
-    *reinterpret_cast<float4*>(row + D + o) = make_float4(acck[4 * q4], acck[4 * q4 + 1], acck[4 * q4 + 2], acck[4 * q4 + 3]);
-  }
+  for (int q4 = 0; q4 < 4; ++q4)
+    *reinterpret_cast<float4*>(row + (q4 < 2 ? m.a : m.b - 8) + 4 * q4) = make_float4(acc[4 * q4], acc[4 * q4 + 1], acc[4 * q4 + 2], acc[4 * q4 + 3]);
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += 256) {
+  for (int c = threadIdx.x; c < D; c += 256) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) v += red[i][c];
-    p.part[(long)blockIdx.x * 2 * D + c] = v;
+    p.part[(long)blockIdx.x * D + c] = v;
   }
 }
 
-// dw[c] = sum over the workgroups' rows, 16 columns a workgroup: 64 threads a float4 column
-// stride over the rows, then add up in LDS, all in a fixed order.
-__global__ __launch_bounds__(256) void k_weight_grad(const float* __restrict__ part, int n, int D, float* dqw, float* dkw) {
-  __shared__ float4 red[64][4];
+// dw[c] = sum over the workgroups' rows of its kind, 16 columns a workgroup: 256 threads a
+// float4 column stride over the rows, then add up in a fixed order.
+__global__ __launch_bounds__(1024) void k_weight_grad(const float* __restrict__ part, int q_wg, int n_wg, int D, float* dqw, float* dkw) {
+  __shared__ float4 red[16][4];
   const int c4 = threadIdx.x & 3, rg = threadIdx.x >> 2;
-  const int col = blockIdx.x * 16 + 4 * c4;
+  const int blocks = D / 16;
+  const bool k = (int)blockIdx.x >= blocks;
+  const int col = (blockIdx.x - (k ? blocks : 0)) * 16 + 4 * c4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int r = rg; r < n; r += 64) {
-    const float4 u = *reinterpret_cast<const float4*>(part + (long)r * 2 * D + col);
+  for (int r = (k ? q_wg : 0) + rg; r < (k ? n_wg : q_wg); r += 256) {
+    const float4 u = *reinterpret_cast<const float4*>(part + (long)r * D + col);
     v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
   }
-  red[rg][c4] = v;
-  __syncthreads();
-  for (int s = 32; s >= 1; s >>= 1) {
-    if (rg < s) {
-      const float4 u = red[rg + s][c4];
-      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-      red[rg][c4] = v;
-    }
-    __syncthreads();
+#pragma unroll
+  for (int d = 4; d < 64; d <<= 1) {
+    v.x += __shfl_xor(v.x, d); v.y += __shfl_xor(v.y, d); v.z += __shfl_xor(v.z, d); v.w += __shfl_xor(v.w, d);
   }
-  if (rg == 0) *reinterpret_cast<float4*>(col < D ? dqw + col : dkw + col - D) = v;
+  if ((threadIdx.x & 63) < 4) red[threadIdx.x >> 6][c4] = v;
+  __syncthreads();
+  if (rg) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) {
+    const float4 u = red[w][c4];
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+  }
+  *reinterpret_cast<float4*>((k ? dkw : dqw) + col) = v;
 }
 
 template <int D, int MODE>
@@ -355,10 +388,14 @@ hipError_t launch_bwd(RopeBwdParams p, hipStream_t s) {
   constexpr int SLOTS = 64 / (D / 16);
   p.rounds_q = (p.n_q + SLOTS - 1) / SLOTS;
   p.rounds_k = (p.n_kv + SLOTS - 1) / SLOTS;
-  p.rounds_v = p.dv ? p.rounds_k : 0;
+  // workgroups of each kind by its rounds, a wave a round at least (the split, and with it the
+  // order of the sums, does not depend on whether dv is given)
+  const int rounds = p.rounds_q + 2 * p.rounds_k;
+  p.q_wg = (int)std::min<long>(std::max(1, ROPE_BWD_WGS * p.rounds_q / rounds), ((long)p.T * p.rounds_q + 3) / 4);
+  p.n_wg = p.q_wg + (int)std::min<long>(ROPE_BWD_WGS - ROPE_BWD_WGS * p.rounds_q / rounds, ((long)p.T * 2 * p.rounds_k + 3) / 4);
   if (p.T > 0) hipLaunchKernelGGL(k_norm_rope_bwd<D>, dim3(p.n_wg), dim3(256), 0, s, p);
   if (p.q_weight)
-    hipLaunchKernelGGL(k_weight_grad, dim3(2 * D / 16), dim3(256), 0, s, p.part, p.n_wg, D, p.dqw, p.dkw);
+    hipLaunchKernelGGL(k_weight_grad, dim3(2 * D / 16), dim3(1024), 0, s, p.part, p.q_wg, p.n_wg, D, p.dqw, p.dkw);
   return hipGetLastError();
 }
 

@@ -85,21 +85,28 @@ __device__ __forceinline__ void ldg_words(const char* p, uint32_t* w) {
 }
 
 // Which of the 8 keys at draft places d0 .. d0 + 7 (negative: before the drafted tokens) the
-// drafted token j of n sees.  mrow: its mask words, or null for the causal rule.
-__device__ __forceinline__ uint32_t visible8(const uint64_t* mrow, int words, int j, int d0, int n) {
+// drafted token j of n sees.  Its mask row: of one word, from LDS (`own`, the sequence's rows;
+// a load from memory would wait for every key and value in flight, which return in order), of
+// more from memory; without a mask, the causal rule.
+__device__ __forceinline__ uint32_t visible8(const TreeAttnParams& p, const uint64_t* own, int q0, int j, int d0, int n) {
   if (d0 <= -8) return 0xffu;
   if (d0 >= n) return 0u;
   uint32_t bits;
-  if (!mrow) {
+  if (!p.mask) {
     const int c = j - d0 + 1;
     bits = c >= 8 ? 0xffu : c <= 0 ? 0u : (1u << c) - 1u;
-  } else if (d0 < 0) {
-    bits = ((uint32_t)mrow[0] << -d0) | ((1u << -d0) - 1u);
   } else {
-    const int w = d0 >> 6, o = d0 & 63;
-    uint64_t v = mrow[w] >> o;
-    if (o > 56 && w + 1 < words) v |= mrow[w + 1] << (64 - o);
+    const int first = max(d0, 0), w = first >> 6, o = first & 63;
+    uint64_t v;
+    if (p.words == 1) {
+      v = own[j] >> o;
+    } else {
+      const uint64_t* row = p.mask + (long)(q0 + j) * p.words;
+      v = row[w] >> o;
+      if (o > 56 && w + 1 < p.words) v |= row[w + 1] << (64 - o);
+    }
     bits = (uint32_t)v;
+    if (d0 < 0) bits = (bits << -d0) | ((1u << -d0) - 1u);
   }
   const int keep = n - d0;
   if (keep < 8) bits &= (1u << keep) - 1u;
@@ -107,155 +114,126 @@ __device__ __forceinline__ uint32_t visible8(const uint64_t* mrow, int words, in
 }
 
 // One sequence: its queries and keys, and how many units and steps they make.
-struct Seq { int q0, n, kv, steps, blocks; bool bad; };
-template <int KEYS>
+struct Seq { int q0, n, kv, steps, blocks, bad; };
 __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1, int kv, int block_rows) {
   Seq s;
   s.q0 = q0;
   s.kv = kv;
-  s.bad = false;
+  s.bad = 0;
   s.n = q1 - q0;
-  if (q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = true; }
-  if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = true; }
-  s.steps = max(1, (s.kv + KEYS - 1) / KEYS);
+  if (q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = 1; }
+  if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = 1; }
+  s.steps = max(1, (s.kv + ATTN_KEYS - 1) / ATTN_KEYS);
   s.blocks = (s.n * p.group + block_rows - 1) / block_rows;
   return s;
 }
 
-// Sum of a value over the workgroup's threads, in every thread (THREADS / 64 words of LDS); and
-// the sum over the threads before this one.
+// A workgroup's stretch [cur, end) of the line of all units' steps, `per` steps a workgroup, and
+// the sequence it begins in, from a prefix sum over the sequences' work that leaves cum[b], the
+// steps before sequence b, in LDS.  (Cutting every unit evenly instead, so that nobody begins a
+// second one, took a search that cost what it saved.)
+struct Stretch { int cur, end, per, b; Seq first; };
 template <int THREADS>
-__device__ __forceinline__ int2 group_scan(int v, int* wave_sum) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int incl = v;
+__device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int* wave_sum,
+                                                Stretch* found) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, each = (p.B + THREADS - 1) / THREADS;
+  int mine = 0;
+  Seq s{};
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    if (b < p.B) {
+      s = make_seq(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
+      if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
+      mine += p.n_kv * s.blocks * s.steps;
+      cum[b + 1] = mine;
+    }
+  }
+  int incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int u = __shfl_up(incl, d);
     if (lane >= d) incl += u;
   }
-  __syncthreads();  // an earlier scan's sums are read
   if (lane == 63) wave_sum[wave] = incl;
+  if (tid == 0) {
+    cum[0] = 0;
+    found->cur = found->end = 0;  // for a workgroup past the end
+  }
   __syncthreads();
-  int before = incl - v, total = 0;
+  int before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) {
     const int u = wave_sum[w];
     before += w < wave ? u : 0;
     total += u;
   }
-  return make_int2(before, total);
-}
-
-// A workgroup's stretch [cur, end) of the line of all units' steps, and the sequence it begins
-// in, found from a prefix sum over the sequences' work that leaves cum[b], the steps before
-// sequence b, in LDS.
-//  - All workgroups take equal stretches of `per` steps, wherever those cut the units
-//    (pieces = 0).
-//  - EVEN, where the units are no more than the workgroups and it makes no piece over 1.5 times
-//    as long: every unit is cut evenly, into as many pieces (`pieces`) as keep the longest
-//    piece shortest with a workgroup each.  Nobody begins a second unit, and most write one
-//    piece, not two (256 rows of 128 values are 128 KB): trees of up to 64 tokens 39 us against
-//    46, but its search costs a few scans: trees of up to 16 tokens 21.5 us against 18.9.
-struct Stretch { int cur, end, b, per, pieces; };
-template <int THREADS, int KEYS, bool EVEN>
-__device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int* wave_sum,
-                                                Stretch* found) {
-  const int tid = threadIdx.x, each = (p.B + THREADS - 1) / THREADS;
-  int mine = 0, units = 0, steps = 1;
+  const int per = (total + p.n_wg - 1) / p.n_wg, cur = min(total, wg * per), end = min(total, cur + per);
+  int from = before;
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
     if (b < p.B) {
-      const Seq s = make_seq<KEYS>(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
-      if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
-      units += p.n_kv * s.blocks;
-      steps = s.steps;
-      mine += p.n_kv * s.blocks * s.steps;
-      cum[b + 1] = mine;
-    }
-  }
-  const int2 work = group_scan<THREADS>(mine, wave_sum);
-  bool even = EVEN && each == 1 && group_scan<THREADS>(min(units, 1 << 20), wave_sum).y <= p.n_wg;
-  if (tid == 0) {
-    cum[0] = 0;
-    found->cur = found->end = 0;
-  }
-  Stretch r;
-  int lo = max(1, (work.y + p.n_wg - 1) / p.n_wg), hi = lo + lo / 2;
-  int2 at;
-  if (even) {
-    at = group_scan<THREADS>(units * ((steps + hi - 1) / hi), wave_sum);
-    even = at.y <= p.n_wg;
-  }
-  if (even) {
-    const int b = tid;
-    // the least c for which pieces of at most c steps are no more than the workgroups
-    while (lo < hi) {
-      const int c = (lo + hi) >> 1;
-      const int2 t = group_scan<THREADS>(units * ((steps + c - 1) / c), wave_sum);
-      if (t.y <= p.n_wg) { hi = c; at = t; } else { lo = c + 1; }
-    }
-    const int k = (steps + hi - 1) / hi;
-    if (b < p.B) {
-      cum[b + 1] += work.x;
-      if (at.x <= wg && wg < at.x + units * k) {
-        const int unit = (wg - at.x) / k, piece = wg - at.x - unit * k;
-        const int base = work.x + unit * steps;
-        *found = Stretch{base + (int)((long)steps * piece / k), base + (int)((long)steps * (piece + 1) / k), b, 1, k};
+      const int next = before + cum[b + 1];
+      if (from <= cur && cur < next) {
+        if (each > 1) s = make_seq(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
+        *found = Stretch{cur, end, per, b, s};
       }
-    }
-  } else {
-    r.per = (work.y + p.n_wg - 1) / p.n_wg;
-    r.cur = min(work.y, wg * r.per);
-    r.end = min(work.y, r.cur + r.per);
-    int from = work.x;
-    for (int i = 0; i < each; ++i) {
-      const int b = tid * each + i;
-      if (b < p.B) {
-        const int next = work.x + cum[b + 1];
-        if (from <= r.cur && r.cur < next) *found = Stretch{r.cur, r.end, b, r.per, 0};
-        cum[b + 1] = next;
-        from = next;
-      }
+      cum[b + 1] = next;
+      from = next;
     }
   }
   __syncthreads();
-  r.cur = __builtin_amdgcn_readfirstlane(found->cur);
-  r.end = __builtin_amdgcn_readfirstlane(found->end);
-  r.b = __builtin_amdgcn_readfirstlane(found->b);
-  r.per = __builtin_amdgcn_readfirstlane(found->per);
-  r.pieces = __builtin_amdgcn_readfirstlane(found->pieces);
-  return r;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  return Stretch{uniform(found->cur), uniform(found->end), uniform(found->per), uniform(found->b),
+                 Seq{uniform(found->first.q0), uniform(found->first.n), uniform(found->first.kv), uniform(found->first.steps),
+                     uniform(found->first.blocks), 0}};
 }
 
-// One row tile's scores of 32 keys (S^T: lane (g, i) has keys 8 g .. 8 g + 7 of row i) into
-// the running softmax; returns the probabilities as the MFMA operand of O^T = V^T P^T.
-template <int NT, bool SPECIAL>
-__device__ __forceinline__ uint4 softmax_step(const v4f (&s)[2], float sc, uint32_t vis, float& m, float& l, v4f (&o)[NT]) {
-  float x[8];  // products of keys 8 g + e; sc >= 0 takes them to log2 units
+// The scores of 32 keys of COUNT row tiles (S^T: lane (g, i) has keys 8 g .. 8 g + 7 of row i)
+// into the running softmax; pb: the probabilities as the MFMA operand of O^T = V^T P^T.
+// m, l, o: the first of the tiles'.
+template <int NT, int COUNT, bool SPECIAL>
+__device__ __forceinline__ void softmax_step(const v4f (&s)[COUNT][2], float sc, const uint32_t (&vis)[COUNT], float* m, float* l,
+                                             v4f (*o)[NT], uint4 (&pb)[COUNT]) {
+  float x[COUNT][8], mx[COUNT];  // products of keys 8 g + e; sc >= 0 takes them to log2 units
+  bool over = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = SPECIAL && !((vis >> e) & 1u) ? NEG_INF : s[e >> 2][e & 3];
-  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), fmaxf(fmaxf(x[3], x[4]), fmaxf(fmaxf(x[5], x[6]), x[7]))) * sc;
-  if (__any(mx > m + SLACK)) {
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    // each row by its own scores alone: what a row gets does not depend on its neighbours
-    const bool up = mx > m + SLACK;
-    const float f = up ? __builtin_amdgcn_exp2f(m - mx) : 1.f;
-    m = up ? mx : m;
-    l *= f;
+  for (int c = 0; c < COUNT; ++c) {
 #pragma unroll
-    for (int tt = 0; tt < NT; ++tt) o[tt] *= f;
+    for (int e = 0; e < 8; ++e) x[c][e] = SPECIAL && !((vis[c] >> e) & 1u) ? NEG_INF : s[c][e >> 2][e & 3];
+    mx[c] = fmaxf(fmaxf(fmaxf(x[c][0], x[c][1]), x[c][2]), fmaxf(fmaxf(x[c][3], x[c][4]), fmaxf(fmaxf(x[c][5], x[c][6]), x[c][7]))) * sc;
+    over |= mx[c] > m[c] + SLACK;
   }
-  const float ref = m == NEG_INF ? 0.f : m;
+  if (__any(over)) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], sc, -ref));
-    if (SPECIAL && !((vis >> e) & 1u)) x[e] = 0.f;  // with a scale of 0, -inf * 0 is no zero
+    for (int c = 0; c < COUNT; ++c) {
+      mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 16));
+      mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 32));
+      // each row by its own scores alone: what a row gets does not depend on its neighbours
+      const bool up = mx[c] > m[c] + SLACK;
+      const float f = up ? __builtin_amdgcn_exp2f(m[c] - mx[c]) : 1.f;
+      m[c] = up ? mx[c] : m[c];
+      l[c] *= f;
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) o[c][tt] *= f;
+    }
+  } else {
+    // a block of its own: without one the compiler copies all of o before the branch, for the
+    // values to be joined after it
+    asm volatile("");
   }
-  l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-  // P enters the MFMA in bf16 (relative error 2^-8 an element at most, as the output's own
-  // rounding); its sum l is taken before the rounding, in 32 bits
-  return make_uint4(bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7]));
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c) {
+    const float ref = m[c] == NEG_INF ? 0.f : m[c];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[c][e], sc, -ref));
+      if (SPECIAL && !((vis[c] >> e) & 1u)) x[c][e] = 0.f;  // with a scale of 0, -inf * 0 is no zero
+    }
+    l[c] += ((x[c][0] + x[c][1]) + (x[c][2] + x[c][3])) + ((x[c][4] + x[c][5]) + (x[c][6] + x[c][7]));
+    // P enters the MFMA in bf16 (relative error 2^-8 an element at most, as the output's own
+    // rounding); its sum l is taken before the rounding, in 32 bits
+    pb[c] = make_uint4(bf16x2_rne(x[c][0], x[c][1]), bf16x2_rne(x[c][2], x[c][3]), bf16x2_rne(x[c][4], x[c][5]), bf16x2_rne(x[c][6], x[c][7]));
+  }
 }
 
 // 8 keys x 2 values in VE-word rows -> the MFMA operand of one value: word w of the rows, its
@@ -406,6 +384,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   __shared__ float sml[4][RT * 16][2];
   __shared__ int wave_sum[4];
   __shared__ Stretch found;
+  __shared__ uint64_t smask[64];  // the sequence's masks, where they are of one word
   // heads of 256: the queries are kept in LDS as operands, their registers hold keys and values
   constexpr bool Q_LDS = D == 256;
   static_assert(!Q_LDS || RT == 1, "one row tile in LDS");
@@ -418,9 +397,10 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   // neighbours, which read the same queries and (row blocks of a unit) the same keys, share an L2
   const int wg = (blockIdx.x & 7) * (p.n_wg >> 3) + (blockIdx.x >> 3);
 
-  const Stretch mine = find_stretch<256, ATTN_KEYS, false>(p, wg, RT * 16, cum, wave_sum, &found);
+  const Stretch mine = find_stretch<256>(p, wg, RT * 16, cum, wave_sum, &found);
   if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
   int cur = mine.cur, b = mine.b;
+  Seq sq = mine.first;
   const int end = mine.end;
 
   const int page = 1 << p.page_log2;
@@ -428,9 +408,8 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   const int voff = 8 * (g & 1) * G::ROWB + i * G::VB;
 
   while (cur < end) {
-    while (cum[b + 1] <= cur) ++b;  // skips sequences without queries
-    b = __builtin_amdgcn_readfirstlane(b);
-    const Seq sq = make_seq<ATTN_KEYS>(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), RT * 16);
+    while (__builtin_amdgcn_readfirstlane(cum[b + 1]) <= cur) ++b;  // skips sequences without queries
+    if (b != mine.b) sq = make_seq(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), RT * 16);
     const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
     const int unit = local / sq.steps, t0 = local - unit * sq.steps;
     const int t1 = min(sq.steps, t0 + end - cur);
@@ -457,7 +436,9 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
         for (int s = 0; s < G::KS; ++s) q[rt][s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
       }
     }
-    if constexpr (Q_LDS) __syncthreads();
+    const bool masks = p.mask && p.words == 1;
+    if (masks && tid < sq.n) smask[tid] = p.mask[sq.q0 + tid];  // words 1: n <= 64
+    if (Q_LDS || masks) __syncthreads();
 
     v4f o[RT][NT];
     float m[RT], l[RT];
@@ -533,14 +514,11 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       const bool gone = g < 2 ? bad0 : bad1;
       uint4 pb[RT];
       uint32_t vis[RT] = {};
+      if constexpr (SPECIAL) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if constexpr (SPECIAL) {
-          const uint64_t* mrow = p.mask ? p.mask + (long)(sq.q0 + jrow[rt]) * p.words : nullptr;
-          vis[rt] = gone ? 0u : visible8(mrow, p.words, jrow[rt], d0, sq.n);
-        }
-        pb[rt] = softmax_step<NT, SPECIAL>(s[rt], sc, vis[rt], m[rt], l[rt], o[rt]);
+        for (int rt = 0; rt < RT; ++rt) vis[rt] = gone ? 0u : visible8(p, smask, sq.q0, jrow[rt], d0, sq.n);
       }
+      softmax_step<NT, RT, SPECIAL>(s, sc, vis, m, l, o, pb);
 
       // V: 8 keys x CH values a lane, widened to bf16
       uint32_t odd = 0;
@@ -642,7 +620,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
-      put_desc(p, wg, mine.pieces ? mine.pieces : (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
+      put_desc(p, wg, (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
     }
     cur += t1 - t0;
   }
@@ -727,40 +705,28 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
   put_row<D>(p, ds.y, ds.w, r, c4, a, M, L, p.v_scale ? p.v_scale[ds.w] : 1.f);
 }
 
-template <typename T>
-__device__ __forceinline__ void swap_regs(T& a, T& b) {
-  const T t = a;
-  a = b;
-  b = t;
-}
-template <typename T, int N>
-__device__ __forceinline__ void swap_regs(T (&a)[N], T (&b)[N]) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) swap_regs(a[k], b[k]);
-}
-
 // The same for many rows (trees of many tokens times a group of heads; a prompt's chunk): eight
-// waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128 RT rows, put into LDS as
+// waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128 rows, put into LDS as
 // MFMA operands (K and the transposed V in bf16, 1 KB a wave's read, conflict free; an 8-bit
-// cache is widened once, here), and each wave takes 16 RT rows through all of them, so nothing
+// cache is widened once, here), and each wave takes 16 rows through all of them, so nothing
 // is joined inside the workgroup.  The next step's loads are in flight, in registers, while a
-// step is computed.  Tiles of 16 rows are dealt to the waves in turn.
+// step is computed.
 // A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
 // of O^T, so that its stores and the join's loads are whole KBs and a wave of the join, which
 // takes one x, has neighbouring values of a row.
 constexpr int ROW_WAVES = 8;
 
-template <int D, int RT, bool FP8>
+template <int D, bool FP8>
 __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeAttnParams p) {
   using G = Geo<D, FP8>;
-  constexpr int NT = D / 16, BLOCK = 16 * RT * ROW_WAVES;
-  constexpr int KEYS = RT == 1 ? ATTN_KEYS : ATTN_SHARED_KEYS;  // of a step: the finer, the more even the pieces
+  constexpr int NT = D / 16, BLOCK = 16 * ROW_WAVES;
   constexpr int VE = G::NCH * G::CH / 2;
   __shared__ uint4 sk[4][2][G::KS][64];  // [32 keys][16 keys][MFMA step][lane]
   __shared__ uint4 sv[4][NT][64];        // [32 keys][tile of O^T][lane]
   __shared__ uint32_t s_odd[4], s_bad[4];
   __shared__ int wave_sum[ROW_WAVES];
   __shared__ Stretch found;
+  __shared__ uint64_t smask[64];  // the sequence's masks, where they are of one word
   extern __shared__ int cum[];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
@@ -769,9 +735,10 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
   const bool loads_v = wave & 1;      // their values, or their keys
   const int wg = (blockIdx.x & 7) * (p.n_wg >> 3) + (blockIdx.x >> 3);
 
-  const Stretch mine = find_stretch<64 * ROW_WAVES, KEYS, RT == 2>(p, wg, BLOCK, cum, wave_sum, &found);
+  const Stretch mine = find_stretch<64 * ROW_WAVES>(p, wg, BLOCK, cum, wave_sum, &found);
   if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
   int cur = mine.cur, b = mine.b;
+  Seq sq = mine.first;
   const int end = mine.end;
 
   const int page = 1 << p.page_log2;
@@ -780,14 +747,13 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
   const bool second = loads_v ? g >= 2 : i >= 8;
 
   while (cur < end) {
-    while (cum[b + 1] <= cur) ++b;
-    b = __builtin_amdgcn_readfirstlane(b);
-    const Seq sq = make_seq<KEYS>(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), BLOCK);
+    while (__builtin_amdgcn_readfirstlane(cum[b + 1]) <= cur) ++b;
+    if (b != mine.b) sq = make_seq(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), BLOCK);
     const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
     const int unit = local / sq.steps, t0 = local - unit * sq.steps;
     const int t1 = min(sq.steps, t0 + end - cur);
     const int h = unit / sq.blocks, rb = unit - h * sq.blocks;
-    constexpr int PER_STEP = KEYS / ATTN_GROUP;
+    constexpr int PER_STEP = ATTN_KEYS / ATTN_GROUP;
     const int g0 = t0 * PER_STEP, g1 = t1 * PER_STEP;  // in groups of 32 keys
     const int rows = sq.n * p.group, prefix = sq.kv - sq.n;
     // without a mask no row of this block sees past its last token
@@ -874,70 +840,64 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
         }
       }
     };
+    uint64_t mask_row = 0;  // words 1: n <= 64
+    if (p.mask && p.words == 1 && tid < sq.n) mask_row = p.mask[sq.q0 + tid];
     fetch(g0);
 
     // scores in log2 units; a negative scale is taken as the queries' sign
     const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = fabsf(scale);
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
-    // queries: row tile rt ROW_WAVES + wave of the block, column i
-    uint4 q[RT][G::KS];
-    int tiles = 0;  // of this wave that hold rows
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = rb * BLOCK + (rt * ROW_WAVES + wave) * 16 + i;
-      if (r - i < rows) tiles = rt + 1;
-      const int j = r / p.group;
+    // queries: row tile `wave` of the block, column i
+    const int row0 = rb * BLOCK + wave * 16;
+    const bool busy = row0 < rows;
+    uint4 q[G::KS];
+    {
+      const int r = row0 + i, j = r / p.group;
       const uint16_t* src = p.q + (long)(sq.q0 + min(j, sq.n - 1)) * p.ldq + (long)(h * p.group + (r - j * p.group)) * D;
 #pragma unroll
-      for (int s = 0; s < G::KS; ++s) q[rt][s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
+      for (int s = 0; s < G::KS; ++s) q[s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
     }
-    v4f o[RT][NT];
-    float m[RT], l[RT];
+    v4f o[1][NT];
+    float m[1] = {NEG_INF}, l[1] = {0.f};
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      m[rt] = NEG_INF;
-      l[rt] = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) o[rt][t] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int t = 0; t < NT; ++t) o[0][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (tid < 64) smask[tid] = mask_row;  // read after the rounds' barriers
 
-    // 32 keys for the first COUNT of the wave's row tiles; SPECIAL: for the tile in the first's
-    // place, which is tile rt0
-    auto group = [&](auto special_t, auto count_t, int gr, int key0, uint32_t bad, int rt0) {
+    // 32 keys; SPECIAL where they reach the drafted ones, the end or a page that does not exist
+    auto group = [&](auto special_t, int gr, int key0, uint32_t bad) {
       constexpr bool SPECIAL = decltype(special_t)::value;
-      constexpr int COUNT = decltype(count_t)::value;
-      v4f s[COUNT][2];
+      // operands come from LDS a window ahead of the products (left alone, the compiler reads
+      // one, waits, and multiplies: 16-token trees 18.0 us against 17.0)
+      // (heads of 256 have no registers for it: one at a time, in pairs of products)
+      constexpr int WIN = 4, KN = 2 * G::KS;
+      constexpr bool AHEAD = D <= 128;
+      uint4 win[AHEAD ? WIN : 1];
+      auto k_at = [&](int n) { return sk[gr][n & 1][n >> 1][lane]; };
+      v4f s[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int rt = 0; rt < COUNT; ++rt) s[rt][0] = s[rt][1] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < G::KS; ++x)
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const uint4 a = sk[gr][kt][x][lane];
-#pragma unroll
-          for (int rt = 0; rt < COUNT; ++rt) s[rt][kt] = mfma_bf16_16x16x32(a, q[rt][x], s[rt][kt]);
-          if (D == 256 && kt == 1) __builtin_amdgcn_sched_barrier(0);  // operands in pairs: all at once spill
-        }
-      uint4 pb[COUNT];
-      uint32_t vis[COUNT] = {};
-#pragma unroll
-      for (int rt = 0; rt < COUNT; ++rt) {
-        if constexpr (SPECIAL) {
-          const int j = min((rb * BLOCK + (rt0 * ROW_WAVES + wave) * 16 + i) / p.group, sq.n - 1);
-          const uint64_t* mrow = p.mask ? p.mask + (long)(sq.q0 + j) * p.words : nullptr;
-          vis[rt] = (bad >> (g >> 1)) & 1u ? 0u : visible8(mrow, p.words, j, key0 + 8 * g - prefix, sq.n);
-        }
-        pb[rt] = softmax_step<NT, SPECIAL>(s[rt], sc, vis[rt], m[rt], l[rt], o[rt]);
+        for (int n = 0; n < WIN; ++n) win[n] = k_at(n);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int n = 0; n < KN; ++n) {
+        s[0][n & 1] = mfma_bf16_16x16x32(AHEAD ? win[n % WIN] : k_at(n), q[n >> 1], s[0][n & 1]);
+        if constexpr (AHEAD) win[n % WIN] = n + WIN < KN ? k_at(n + WIN) : sv[gr][n + WIN - KN][lane];  // then the values' first
+        if (AHEAD || (n & 1)) __builtin_amdgcn_sched_barrier(0);
+      }
+      uint4 pb[1];
+      uint32_t vis[1] = {0};
+      if constexpr (SPECIAL)
+        vis[0] = (bad >> (g >> 1)) & 1u ? 0u : visible8(p, smask, sq.q0, min((row0 + i) / p.group, sq.n - 1), key0 + 8 * g - prefix, sq.n);
+      softmax_step<NT, 1, SPECIAL>(s, sc, vis, m, l, o, pb);
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt) {
-        const uint4 a = sv[gr][tt][lane];
-#pragma unroll
-        for (int rt = 0; rt < COUNT; ++rt) o[rt][tt] = mfma_bf16_16x16x32(a, pb[rt], o[rt][tt]);
-        if (D == 256 && (tt & 1)) __builtin_amdgcn_sched_barrier(0);
+        o[0][tt] = mfma_bf16_16x16x32(AHEAD ? win[(KN + tt) % WIN] : sv[gr][tt][lane], pb[0], o[0][tt]);
+        if constexpr (AHEAD)
+          if (tt + WIN < NT) win[(KN + tt) % WIN] = sv[gr][tt + WIN][lane];
+        if (AHEAD || (tt & 1)) __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (SPECIAL) {
-        static_assert(COUNT == 1, "one row tile at a time");
         const uint32_t odd = __builtin_amdgcn_readfirstlane((int)s_odd[gr]);
         if (odd) {
           auto at = [&](int key) {
@@ -948,7 +908,6 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
         }
       }
     };
-    using std::integral_constant;
 
     for (int t = g0; t < g1; t += 4) {
       __syncthreads();  // the round before is read
@@ -957,66 +916,47 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       __syncthreads();
       for (int gr = 0; gr < 4 && t + gr < g1; ++gr) {
         const int key0 = (t + gr) * ATTN_GROUP;
-        if (key0 >= kv || tiles == 0) break;
+        if (key0 >= kv || !busy) break;
         const uint32_t bad = __builtin_amdgcn_readfirstlane((int)s_bad[gr]);
-        if (key0 + 32 > prefix || bad) {
-          // one row tile at a time, each in the first's registers: these few groups' code for
-          // two would spill
-          for (int rt0 = 0; rt0 < tiles; ++rt0) {
-            group(std::true_type{}, integral_constant<int, 1>{}, gr, key0, bad, rt0);
-            if constexpr (RT == 2) {
-              if (tiles == 2) {
-                swap_regs(q[0], q[1]);
-                swap_regs(o[0], o[1]);
-                swap_regs(m[0], m[1]);
-                swap_regs(l[0], l[1]);
-              }
-            }
-          }
-        } else if (tiles == RT) {
-          group(std::false_type{}, integral_constant<int, RT>{}, gr, key0, 0, 0);
-        } else {
-          group(std::false_type{}, integral_constant<int, 1>{}, gr, key0, 0, 0);
-        }
+        if (key0 + 32 > prefix || bad)
+          group(std::true_type{}, gr, key0, bad);
+        else
+          group(std::false_type{}, gr, key0, 0);
       }
     }
 
     const bool whole = t0 == 0 && t1 == sq.steps;
     const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
-    const float vs = FP8 ? p.v_scale[h] : 1.f;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if (rt >= tiles) break;
-      const int tile = rt * ROW_WAVES + wave, r = rb * BLOCK + tile * 16 + i;
-      l[rt] += __shfl_xor(l[rt], 16);
-      l[rt] += __shfl_xor(l[rt], 32);
+    if (busy) {
+      l[0] += __shfl_xor(l[0], 16);
+      l[0] += __shfl_xor(l[0], 32);
       if (whole) {
-        put_tile<D, G::CH>(p, sq.q0, rows, h, r, g, o[rt], m[rt], l[rt], vs);
+        put_tile<D, G::CH>(p, sq.q0, rows, h, row0 + i, g, o[0], m[0], l[0], FP8 ? p.v_scale[h] : 1.f);
       } else {
-        float* dst = p.part_o + ((long)slot * (BLOCK / 16) + tile) * (16 * D) + 4 * lane;
+        float* dst = p.part_o + ((long)slot * (BLOCK / 16) + wave) * (16 * D) + 4 * lane;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int t4 = 0; t4 < NT; t4 += 4)
             *reinterpret_cast<float4*>(dst + (x * (NT / 4) + t4 / 4) * 256) =
-                make_float4(o[rt][t4][x], o[rt][t4 + 1][x], o[rt][t4 + 2][x], o[rt][t4 + 3][x]);
-        if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + tile * 16 + i)) = make_float2(m[rt], l[rt]);
+                make_float4(o[0][t4][x], o[0][t4 + 1][x], o[0][t4 + 2][x], o[0][t4 + 3][x]);
+        if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + wave * 16 + i)) = make_float2(m[0], l[0]);
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
-      put_desc(p, wg, mine.pieces ? mine.pieces : (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
+      put_desc(p, wg, (cur + sq.steps - 1) / mine.per - wg + 1, sq, h, rb);
     }
     cur += t1 - t0;
   }
 }
 
 // Joins the pieces of k_tree_attention_rows: a workgroup a row tile, a wave one x of it.  The
-// pieces are taken four at a time with a running maximum, so that all loads of a round, the
+// pieces are taken KR at a time with a running maximum, so that all loads of a round, the
 // pieces' (m, l) among them, are in flight together: the launch is a chain of latencies (a
 // pass of its own over the maxima, and a wave for a whole tile, took 10.8 us at 64 rows).
 template <int D, int CH>
 __global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int block_rows) {
-  constexpr int NV = D / 64;  // float4 of a lane
+  constexpr int NV = D / 64, KR = D == 256 ? 4 : 8;  // float4 of a lane; pieces of a round
   const int wg = blockIdx.x, tile = blockIdx.y;
   const int4 ds = *reinterpret_cast<const int4*>(p.desc + ATTN_DESC * wg);
   const int rb = p.desc[ATTN_DESC * wg + 4];
@@ -1030,11 +970,11 @@ __global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int
   float4 o[NV];
 #pragma unroll
   for (int t = 0; t < NV; ++t) o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < ds.x; k0 += 4) {
-    float2 v[4];
-    float4 u[4][NV];
+  for (int k0 = 0; k0 < ds.x; k0 += KR) {
+    float2 v[KR];
+    float4 u[KR][NV];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < KR; ++k) {
       const int kk = min(k0 + k, ds.x - 1);  // the last piece again, with no weight
       const long slot = kk == 0 ? 2 * wg + 1 : 2 * (wg + kk);
       v[k] = *reinterpret_cast<const float2*>(ml + 2 * slot * block_rows);
@@ -1043,14 +983,14 @@ __global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int
     }
     float mn = M;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, v[k].x);
+    for (int k = 0; k < KR; ++k) mn = fmaxf(mn, v[k].x);
     const float back = M == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(M - mn);
     L *= back;
 #pragma unroll
     for (int t = 0; t < NV; ++t) { o[t].x *= back; o[t].y *= back; o[t].z *= back; o[t].w *= back; }
     M = mn;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < KR; ++k) {
       // selected, not branched around: a branch would pull the loads apart, one wait each
       const bool real = k0 + k < ds.x;
       const float f = v[k].x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(v[k].x - M);
@@ -1116,10 +1056,10 @@ void launch_few(const TreeAttnParams& p, hipStream_t s) {
     hipLaunchKernelGGL((k_tree_combine<D, false>), dim3(p.n_wg, (rows + 3) / 4), dim3(256), 0, s, p, RT * 16);
 }
 
-template <int D, int RT, bool FP8>
+template <int D, bool FP8>
 void launch_rows(const TreeAttnParams& p, hipStream_t s) {
-  constexpr int BLOCK = 16 * RT * ROW_WAVES;
-  hipLaunchKernelGGL((k_tree_attention_rows<D, RT, FP8>), dim3(p.n_wg), dim3(64 * ROW_WAVES), (p.B + 1) * sizeof(int), s, p);
+  constexpr int BLOCK = 16 * ROW_WAVES;
+  hipLaunchKernelGGL((k_tree_attention_rows<D, FP8>), dim3(p.n_wg), dim3(64 * ROW_WAVES), (p.B + 1) * sizeof(int), s, p);
   const long rows = min((long)BLOCK, (long)p.max_q * p.group);
   hipLaunchKernelGGL((k_tree_combine_rows<D, Geo<D, FP8>::CH>), dim3(p.n_wg, (unsigned)((rows + 15) / 16)), dim3(256), 0, s, p, BLOCK);
 }
@@ -1127,12 +1067,7 @@ void launch_rows(const TreeAttnParams& p, hipStream_t s) {
 template <int D, bool FP8>
 hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t s) {
   if (pl.shared) {
-    if constexpr (D <= 128) {
-      if (pl.row_tiles == 1) launch_rows<D, 1, FP8>(p, s);
-      else launch_rows<D, 2, FP8>(p, s);
-    } else if constexpr (FP8) {
-      launch_rows<D, 1, FP8>(p, s);
-    }
+    if constexpr (D <= 128 || FP8) launch_rows<D, FP8>(p, s);
   } else {
     if (pl.row_tiles == 1) launch_few<D, 1, FP8>(p, s);
     else if constexpr (D <= 128) launch_few<D, 2, FP8>(p, s);
@@ -1147,8 +1082,8 @@ TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   // 16-bit heads of 256 do not fit the registers of a wave that also holds a step's loads
   pl.shared = rows > (D > 128 ? 16 : 32) && (D <= 128 || fp8);
   if (pl.shared) {
-    pl.row_tiles = rows <= 16 * ROW_WAVES || D > 128 ? 1 : 2;
-    pl.block_rows = 16 * ROW_WAVES * pl.row_tiles;
+    pl.row_tiles = 1;
+    pl.block_rows = 16 * ROW_WAVES;
     pl.n_wg = 256;
   } else {
     pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;

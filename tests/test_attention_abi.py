@@ -57,7 +57,7 @@ def test_append(L, kw, status):
 
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(dq=NULL), INVALID), (dict(dk=ODD), INVALID), (dict(dv=ODD), INVALID), (dict(out=NULL), INVALID), (dict(ldd=100), INVALID),
-    (dict(dqw=NULL), INVALID), (dict(dkw=ODD), INVALID), (dict(), WORKSPACE), (dict(ws=FAKE, wsb=100), WORKSPACE),
+    (dict(dqw=NULL), INVALID), (dict(dkw=ODD), INVALID), (dict(), WORKSPACE), (dict(ws=FAKE, wsb=1000), WORKSPACE),
     (dict(ws=ODD, wsb=1 << 20), WORKSPACE)])
 def test_backward(L, kw, status):
     base = dict(ROPE, dq=FAKE, dk=FAKE, dv=FAKE, out=FAKE, ldd=768, dqw=FAKE, dkw=FAKE, ws=NULL, wsb=0)
@@ -67,7 +67,7 @@ def test_backward(L, kw, status):
 
 def test_backward_workspace_bytes(L):
     f = L.lora_qk_norm_rope_backward_workspace_bytes
-    assert f(1, 64) == 512 and f(65536, 256) == 1024 * 2048 and f(0, 64) == 0 and f(5, 96) == 0 and f(70000, 64) == 0
+    assert f(1, 64) == 768 * 256 and f(65536, 256) == 768 * 1024 and f(0, 64) == 0 and f(5, 96) == 0 and f(70000, 64) == 0
 
 
 @pytest.mark.parametrize("kw,status", [
