@@ -304,10 +304,11 @@ __device__ __forceinline__ uint32_t clean_v(uint32_t (&row)[8][W], int g, bool g
 }
 
 // The keys that clean_v took out (bit 8 g + e of `odd`), one at a time: each as the operand
-// whose only key it is, its product added to the rows that see it.
-template <int D, bool FP8>
+// whose only key it is, its product added to the rows that see it.  In part `part` of PARTS of
+// the tiles of O^T, where the rows were cleaned in parts.
+template <int D, bool FP8, int PARTS = 1>
 __device__ __forceinline__ void add_odd_keys(uint32_t odd, const char* v0, const char* v1, const uint4& pb, uint32_t vis,
-                                             v4f (&o)[D / 16]) {
+                                             v4f (&o)[D / 16], int part = 0) {
   using G = Geo<D, FP8>;
   constexpr int VE = G::NCH * G::CH / 2;
   const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
@@ -322,6 +323,7 @@ __device__ __forceinline__ void add_odd_keys(uint32_t odd, const char* v0, const
     const bool sees = (__shfl((int)vis, 16 * gk + i) >> e) & 1;
 #pragma unroll
     for (int tt = 0; tt < D / 16; ++tt) {
+      if (PARTS > 1 && tt / (D / 16 / PARTS) != part) continue;
       const uint32_t half = (v[tt >> 1] >> (16 * (tt & 1))) & 0xffffu;
       const uint32_t val = g == gk ? half << (16 * (e & 1)) : 0u;
       const uint4 a = make_uint4((e >> 1) == 0 ? val : 0u, (e >> 1) == 1 ? val : 0u, (e >> 1) == 2 ? val : 0u, (e >> 1) == 3 ? val : 0u);
@@ -708,9 +710,9 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
 // The same for many rows (trees of many tokens times a group of heads; a prompt's chunk): eight
 // waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128 rows, put into LDS as
 // MFMA operands (K and the transposed V in bf16, 1 KB a wave's read, conflict free; an 8-bit
-// cache is widened once, here), and each wave takes 16 rows through all of them, so nothing
-// is joined inside the workgroup.  The next step's loads are in flight, in registers, while a
-// step is computed.
+// cache is widened once, here), and each wave takes 16 rows through all of them; of 64 rows
+// or fewer, two or four waves share each 16 (32 sequences of 2,048 keys, 64 rows: 61 us against
+// 70).  The next round's loads are in flight, in registers, while one is computed.
 // A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
 // of O^T, so that its stores and the join's loads are whole KBs and a wave of the join, which
 // takes one x, has neighbouring values of a row.
@@ -720,10 +722,21 @@ template <int D, bool FP8>
 __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeAttnParams p) {
   using G = Geo<D, FP8>;
   constexpr int NT = D / 16, BLOCK = 16 * ROW_WAVES;
+  // a round's groups of 32 keys, the waves that load one, and a wave's words of a key: half a
+  // group's K or V (heads of 256: a quarter), 8 to 32 registers
+  constexpr int GR = D == 256 ? 2 : 4, PARTS = ROW_WAVES / GR, SW = G::NCH * G::VW / (PARTS / 2);
+  static_assert(2 * G::KL / (PARTS / 2) == 2 * SW, "keys and values take the same registers");
+  // V in parts: by a lane's loads of a key, or within its one load
+  constexpr int LOADS = PARTS == 2 ? G::NCH : 1, LOAD_BYTES = 4 * SW / LOADS;
+  constexpr int PART_BYTES = G::NCH > 1 ? 16 * G::VB : LOAD_BYTES;
   constexpr int VE = G::NCH * G::CH / 2;
-  __shared__ uint4 sk[4][2][G::KS][64];  // [32 keys][16 keys][MFMA step][lane]
-  __shared__ uint4 sv[4][NT][64];        // [32 keys][tile of O^T][lane]
-  __shared__ uint32_t s_odd[4], s_bad[4];
+  // a round's operands: K [32 keys][16 keys][MFMA step][lane], V [32 keys][tile of O^T][lane]; at
+  // a unit's end, accumulators to be joined
+  __shared__ uint4 ops[GR * 2 * G::KS * 64 + GR * NT * 64];
+  auto sk = [&](int gr, int kt, int step) -> uint4& { return ops[((gr * 2 + kt) * G::KS + step) * 64 + (threadIdx.x & 63)]; };
+  auto sv = [&](int gr, int tile) -> uint4& { return ops[GR * 2 * G::KS * 64 + (gr * NT + tile) * 64 + (threadIdx.x & 63)]; };
+  __shared__ uint32_t s_odd[GR][PARTS / 2], s_bad[GR];
+  __shared__ float2 sml[ROW_WAVES][16];
   __shared__ int wave_sum[ROW_WAVES];
   __shared__ Stretch found;
   __shared__ uint64_t smask[64];  // the sequence's masks, where they are of one word
@@ -731,8 +744,9 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = wave >> 1;          // the 32 keys of a step this wave loads
-  const bool loads_v = wave & 1;      // their values, or their keys
+  const int grp = wave / PARTS;                      // the 32 keys of a round this wave loads,
+  const bool loads_v = wave % PARTS >= PARTS / 2;    // their values or their keys,
+  const int part = wave % PARTS % (PARTS / 2);       // and which of those
   const int wg = (blockIdx.x & 7) * (p.n_wg >> 3) + (blockIdx.x >> 3);
 
   const Stretch mine = find_stretch<64 * ROW_WAVES>(p, wg, BLOCK, cum, wave_sum, &found);
@@ -743,7 +757,8 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
 
   const int page = 1 << p.page_log2;
   // this lane's first byte of a half of 16 keys, and which half it loads
-  const int off = loads_v ? 8 * (g & 1) * G::ROWB + i * G::VB : (8 * ((i >> 2) & 1) + (i & 3)) * G::ROWB + 16 * g;
+  const int off = loads_v ? 8 * (g & 1) * G::ROWB + i * G::VB + part * PART_BYTES
+                          : (8 * ((i >> 2) & 1) + (i & 3) + 4 * part) * G::ROWB + 16 * g;
   const bool second = loads_v ? g >= 2 : i >= 8;
 
   while (cur < end) {
@@ -754,87 +769,82 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     const int t1 = min(sq.steps, t0 + end - cur);
     const int h = unit / sq.blocks, rb = unit - h * sq.blocks;
     constexpr int PER_STEP = ATTN_KEYS / ATTN_GROUP;
-    const int g0 = t0 * PER_STEP, g1 = t1 * PER_STEP;  // in groups of 32 keys
     const int rows = sq.n * p.group, prefix = sq.kv - sq.n;
     // without a mask no row of this block sees past its last token
     const int last_row = min(rows, (rb + 1) * BLOCK) - 1;
     const int kv = p.mask ? sq.kv : min(sq.kv, prefix + last_row / p.group + 1);
     const int* table = p.page_table + (long)b * p.max_pages;
+    const int g0 = t0 * PER_STEP, g1 = min(t1 * PER_STEP, (kv + ATTN_GROUP - 1) / ATTN_GROUP);  // groups of 32 keys
 
-    // this wave's loads of a step: V [8 keys][words], or K [16 keys][load] in the same words
-    constexpr int SW = G::NCH * G::VW;
-    static_assert(2 * G::KL * 4 == 8 * SW, "keys and values take the same registers");
-    uint32_t st[8][SW];
-    auto kw = [&](int kt, int c, int x) -> uint32_t& { return st[(4 * (kt * G::KL + c) + x) / SW][(4 * (kt * G::KL + c) + x) % SW]; };
-    int id0 = 0, id1 = 0;
-    auto fetch = [&](int t) {  // a round: up to four groups from t on
-      const int key = (t + grp) * ATTN_GROUP;
-      if (t + grp >= g1 || key >= kv) return;
+    // this wave's loads of a round: V [8 keys][words], or K [load] in the same words (a second
+    // round in flight measured slower: 16-token trees 19.7 us against 17.1)
+    struct { uint32_t w[8][SW]; int id0, id1; } ld;
+    auto fetch = [&](int t) {  // a round: up to GR groups from t on (past the last: that one again)
+      const int key = min(t + grp, g1 - 1) * ATTN_GROUP;
       const int last = (sq.kv - 1) >> p.page_log2;
-      id0 = ld_table(table + min(key >> p.page_log2, last));
-      id1 = ld_table(table + min((key + 16) >> p.page_log2, last));
+      ld.id0 = ld_table(table + min(key >> p.page_log2, last));
+      ld.id1 = ld_table(table + min((key + 16) >> p.page_log2, last));
       auto base = [&](int id, int k) {
         const int ok = (unsigned)id < (unsigned)p.n_pages ? id : 0;
         return ((((long)ok * p.n_kv + h) << p.page_log2) + (k & (page - 1))) * G::ROWB;
       };
-      const long b0 = base(id0, key), b1 = base(id1, key + 16);
+      const long b0 = base(ld.id0, key), b1 = base(ld.id1, key + 16);
+      const char* src = reinterpret_cast<const char*>(loads_v ? p.v_cache : p.k_cache) + (second ? b1 : b0) + off;
       if (loads_v) {
-        const char* src = reinterpret_cast<const char*>(p.v_cache) + (second ? b1 : b0) + off;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
-          for (int c = 0; c < G::NCH; ++c) ldg_words<G::VB>(src + e * G::ROWB + c * 16 * G::VB, &st[e][c * G::VW]);
+          for (int c = 0; c < LOADS; ++c) ldg_words<LOAD_BYTES>(src + e * G::ROWB + c * 16 * G::VB, &ld.w[e][c * LOAD_BYTES / 4]);
       } else {
-        const char* src = reinterpret_cast<const char*>(p.k_cache) + (second ? b1 : b0) + off;
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int c = 0; c < G::KL; ++c) {
-            const uint4 w = ldg16(src + kt * 4 * G::ROWB + 64 * c);
-            kw(kt, c, 0) = w.x; kw(kt, c, 1) = w.y; kw(kt, c, 2) = w.z; kw(kt, c, 3) = w.w;
-          }
+        for (int n = 0; n < 2 * SW; ++n) {  // 16-byte load n: subtile n / KL of this wave's, piece n % KL
+          const uint4 w = ldg16(src + (n / G::KL) * 4 * G::ROWB + 64 * (n % G::KL));
+          ld.w[4 * n / SW][4 * n % SW] = w.x; ld.w[(4 * n + 1) / SW][(4 * n + 1) % SW] = w.y;
+          ld.w[(4 * n + 2) / SW][(4 * n + 2) % SW] = w.z; ld.w[(4 * n + 3) / SW][(4 * n + 3) % SW] = w.w;
+        }
       }
     };
     auto stage = [&](int t) {
-      const int key = (t + grp) * ATTN_GROUP;
-      if (t + grp >= g1 || key >= kv) return;
-      const bool bad0 = (unsigned)id0 >= (unsigned)p.n_pages, bad1 = (unsigned)id1 >= (unsigned)p.n_pages;
+      const int key = min(t + grp, g1 - 1) * ATTN_GROUP;
+      const bool bad0 = (unsigned)ld.id0 >= (unsigned)p.n_pages, bad1 = (unsigned)ld.id1 >= (unsigned)p.n_pages;
       if (loads_v) {
         uint32_t odd = 0;
         if (key + 32 > prefix || bad0 || bad1) {
-          const uint32_t mine = clean_v<FP8>(st, g, g < 2 ? bad0 : bad1, key + 8 * g - prefix, sq.n);
+          const uint32_t mine = clean_v<FP8>(ld.w, g, g < 2 ? bad0 : bad1, key + 8 * g - prefix, sq.n);
 #pragma unroll
           for (int gk = 0; gk < 4; ++gk) odd |= (uint32_t)__builtin_amdgcn_readlane((int)mine, 16 * gk) << (8 * gk);
         }
-        if (lane == 0) s_odd[grp] = odd;
+        if (lane == 0) s_odd[grp][part] = odd;
+        const int tile0 = part * (NT / (PARTS / 2));
         if constexpr (FP8) {  // a word of the eight rows at a time: four tiles
 #pragma unroll
           for (int w = 0; w < SW; ++w) {
             uint32_t vb[8][2];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const uint2 u = fp8x4_to_bf16(st[e][w]);
+              const uint2 u = fp8x4_to_bf16(ld.w[e][w]);
               vb[e][0] = u.x;
               vb[e][1] = u.y;
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sv[grp][4 * w + x][lane] = transposed<2>(vb, x >> 1, x & 1);
+            for (int x = 0; x < 4; ++x) sv(grp, tile0 + 4 * w + x) = transposed<2>(vb, x >> 1, x & 1);
             __builtin_amdgcn_sched_barrier(0);
           }
         } else {
 #pragma unroll
-          for (int tt = 0; tt < NT; ++tt) sv[grp][tt][lane] = transposed<VE>(st, tt >> 1, tt & 1);
+          for (int tt = 0; tt < 2 * SW; ++tt) sv(grp, tile0 + tt) = transposed<SW>(ld.w, tt >> 1, tt & 1);
         }
       } else {
+        uint4 kr[2 * SW];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          uint4 kr[G::KL];
+        for (int n = 0; n < 2 * SW; ++n)
+          kr[n] = make_uint4(ld.w[4 * n / SW][4 * n % SW], ld.w[(4 * n + 1) / SW][(4 * n + 1) % SW],
+                             ld.w[(4 * n + 2) / SW][(4 * n + 2) % SW], ld.w[(4 * n + 3) / SW][(4 * n + 3) % SW]);
 #pragma unroll
-          for (int c = 0; c < G::KL; ++c) kr[c] = make_uint4(kw(kt, c, 0), kw(kt, c, 1), kw(kt, c, 2), kw(kt, c, 3));
+        for (int n = 0; n < 2 * SW / G::KL; ++n)
 #pragma unroll
-          for (int s = 0; s < G::KS; ++s) sk[grp][kt][s][lane] = k_operand<FP8>(kr, s);
-        }
-        if (lane == 0) {
+          for (int s = 0; s < G::KS; ++s) sk(grp, part + n, s) = k_operand<FP8>(kr + n * G::KL, s);
+        if (lane == 0 && part == 0) {
           s_bad[grp] = (bad0 ? 1u : 0u) | (bad1 ? 2u : 0u);
           if ((bad0 || bad1) && p.status) or_agent(p.status, ST_PAGE);
         }
@@ -842,13 +852,17 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     };
     uint64_t mask_row = 0;  // words 1: n <= 64
     if (p.mask && p.words == 1 && tid < sq.n) mask_row = p.mask[sq.q0 + tid];
-    fetch(g0);
+    if (g0 < g1) fetch(g0);
 
     // scores in log2 units; a negative scale is taken as the queries' sign
     const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = fabsf(scale);
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
-    // queries: row tile `wave` of the block, column i
-    const int row0 = rb * BLOCK + wave * 16;
+    // Eight row tiles of 16, a wave each; of four or fewer (two or fewer), two (four) waves take
+    // each, with the groups of a round between them.
+    const int left = rows - rb * BLOCK, split = left <= 32 && GR == 4 ? 4 : left <= 64 ? 2 : 1;
+    const int tiles = ROW_WAVES / split, tile = wave % tiles, mine_of = wave / tiles;
+    // queries: column i of the tile
+    const int row0 = rb * BLOCK + tile * 16;
     const bool busy = row0 < rows;
     uint4 q[G::KS];
     {
@@ -872,7 +886,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       constexpr int WIN = 4, KN = 2 * G::KS;
       constexpr bool AHEAD = D <= 128;
       uint4 win[AHEAD ? WIN : 1];
-      auto k_at = [&](int n) { return sk[gr][n & 1][n >> 1][lane]; };
+      auto k_at = [&](int n) { return sk(gr, n & 1, n >> 1); };
       v4f s[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
       if constexpr (AHEAD) {
 #pragma unroll
@@ -882,7 +896,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
 #pragma unroll
       for (int n = 0; n < KN; ++n) {
         s[0][n & 1] = mfma_bf16_16x16x32(AHEAD ? win[n % WIN] : k_at(n), q[n >> 1], s[0][n & 1]);
-        if constexpr (AHEAD) win[n % WIN] = n + WIN < KN ? k_at(n + WIN) : sv[gr][n + WIN - KN][lane];  // then the values' first
+        if constexpr (AHEAD) win[n % WIN] = n + WIN < KN ? k_at(n + WIN) : sv(gr, n + WIN - KN);  // then the values' first
         if (AHEAD || (n & 1)) __builtin_amdgcn_sched_barrier(0);
       }
       uint4 pb[1];
@@ -892,31 +906,33 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       softmax_step<NT, 1, SPECIAL>(s, sc, vis, m, l, o, pb);
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt) {
-        o[0][tt] = mfma_bf16_16x16x32(AHEAD ? win[(KN + tt) % WIN] : sv[gr][tt][lane], pb[0], o[0][tt]);
+        o[0][tt] = mfma_bf16_16x16x32(AHEAD ? win[(KN + tt) % WIN] : sv(gr, tt), pb[0], o[0][tt]);
         if constexpr (AHEAD)
-          if (tt + WIN < NT) win[(KN + tt) % WIN] = sv[gr][tt + WIN][lane];
+          if (tt + WIN < NT) win[(KN + tt) % WIN] = sv(gr, tt + WIN);
         if (AHEAD || (tt & 1)) __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (SPECIAL) {
-        const uint32_t odd = __builtin_amdgcn_readfirstlane((int)s_odd[gr]);
-        if (odd) {
-          auto at = [&](int key) {
-            const int id = ld_table(table + (key >> p.page_log2));  // a page that exists: its keys are seen
-            return reinterpret_cast<const char*>(p.v_cache) + ((((long)id * p.n_kv + h) << p.page_log2) + (key & (page - 1))) * G::ROWB;
-          };
-          add_odd_keys<D, FP8>(odd, odd & 0xffffu ? at(key0) : nullptr, odd >> 16 ? at(key0 + 16) : nullptr, pb[0], vis[0], o[0]);
+#pragma unroll
+        for (int part = 0; part < PARTS / 2; ++part) {
+          const uint32_t odd = __builtin_amdgcn_readfirstlane((int)s_odd[gr][part]);
+          if (odd) {
+            auto at = [&](int key) {
+              const int id = ld_table(table + (key >> p.page_log2));  // a page that exists: its keys are seen
+              return reinterpret_cast<const char*>(p.v_cache) + ((((long)id * p.n_kv + h) << p.page_log2) + (key & (page - 1))) * G::ROWB;
+            };
+            add_odd_keys<D, FP8, PARTS / 2>(odd, odd & 0xffffu ? at(key0) : nullptr, odd >> 16 ? at(key0 + 16) : nullptr, pb[0], vis[0], o[0], part);
+          }
         }
       }
     };
 
-    for (int t = g0; t < g1; t += 4) {
+    for (int t = g0; t < g1; t += GR) {
       __syncthreads();  // the round before is read
       stage(t);
-      if (t + 4 < g1) fetch(t + 4);
+      if (t + GR < g1) fetch(t + GR);
       __syncthreads();
-      for (int gr = 0; gr < 4 && t + gr < g1; ++gr) {
+      for (int gr = mine_of; gr < GR && t + gr < g1 && busy; gr += split) {
         const int key0 = (t + gr) * ATTN_GROUP;
-        if (key0 >= kv || !busy) break;
         const uint32_t bad = __builtin_amdgcn_readfirstlane((int)s_bad[gr]);
         if (key0 + 32 > prefix || bad)
           group(std::true_type{}, gr, key0, bad);
@@ -927,20 +943,44 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
 
     const bool whole = t0 == 0 && t1 == sq.steps;
     const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
-    if (busy) {
-      l[0] += __shfl_xor(l[0], 16);
-      l[0] += __shfl_xor(l[0], 32);
+    l[0] += __shfl_xor(l[0], 16);
+    l[0] += __shfl_xor(l[0], 32);
+    if (split > 1) {  // join the waves of a tile, in order, in the first of them
+      v4f* so = reinterpret_cast<v4f*>(ops);
+      __syncthreads();  // the last round is read
+      if (mine_of) {
+        const int at = (wave - tiles) * NT;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) so[(at + tt) * 64 + lane] = o[0][tt];
+        if (g == 0) sml[wave][i] = make_float2(m[0], l[0]);
+      }
+      __syncthreads();
+      if (mine_of == 0) {
+        for (int w = 1; w < split; ++w) {
+          const float2 ml = sml[tile + w * tiles][i];
+          const float mn = fmaxf(m[0], ml.x);
+          const float f = m[0] == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m[0] - mn);
+          const float fw = ml.x == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml.x - mn);
+          const int at = (tile + (w - 1) * tiles) * NT;
+          m[0] = mn;
+          l[0] = l[0] * f + ml.y * fw;
+#pragma unroll
+          for (int tt = 0; tt < NT; ++tt) o[0][tt] = o[0][tt] * f + so[(at + tt) * 64 + lane] * fw;
+        }
+      }
+    }
+    if (busy && mine_of == 0) {
       if (whole) {
         put_tile<D, G::CH>(p, sq.q0, rows, h, row0 + i, g, o[0], m[0], l[0], FP8 ? p.v_scale[h] : 1.f);
       } else {
-        float* dst = p.part_o + ((long)slot * (BLOCK / 16) + wave) * (16 * D) + 4 * lane;
+        float* dst = p.part_o + ((long)slot * (BLOCK / 16) + tile) * (16 * D) + 4 * lane;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int t4 = 0; t4 < NT; t4 += 4)
             *reinterpret_cast<float4*>(dst + (x * (NT / 4) + t4 / 4) * 256) =
                 make_float4(o[0][t4][x], o[0][t4 + 1][x], o[0][t4 + 2][x], o[0][t4 + 3][x]);
-        if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + wave * 16 + i)) = make_float2(m[0], l[0]);
+        if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + tile * 16 + i)) = make_float2(m[0], l[0]);
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
@@ -1067,10 +1107,10 @@ void launch_rows(const TreeAttnParams& p, hipStream_t s) {
 template <int D, bool FP8>
 hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t s) {
   if (pl.shared) {
-    if constexpr (D <= 128 || FP8) launch_rows<D, FP8>(p, s);
+    launch_rows<D, FP8>(p, s);
   } else {
     if (pl.row_tiles == 1) launch_few<D, 1, FP8>(p, s);
-    else if constexpr (D <= 128) launch_few<D, 2, FP8>(p, s);
+    else if constexpr (D <= 128 && FP8) launch_few<D, 2, FP8>(p, s);
   }
   return hipGetLastError();
 }
@@ -1079,8 +1119,10 @@ hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t
 
 TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   TreeAttnPlan pl;
-  // 16-bit heads of 256 do not fit the registers of a wave that also holds a step's loads
-  pl.shared = rows > (D > 128 ? 16 : 32) && (D <= 128 || fp8);
+  // 17 to 32 rows of an 8-bit cache: waves that split the keys, with two tiles of rows, do not
+  // put what they widen through LDS (32 sequences of 2,048 keys, 32 rows: 40 us against 48; in
+  // 16 bits 58 against 55)
+  pl.shared = rows > (fp8 && D <= 128 ? 32 : 16);
   if (pl.shared) {
     pl.row_tiles = 1;
     pl.block_rows = 16 * ROW_WAVES;
