@@ -29,8 +29,7 @@ struct RopeParams {
   int page_log2;
   long n_slots;
   int* status;
-  int rounds_q, rounds_k, rounds_v;  // rounds of one wave over the heads of each kind
-  int per_wave, groups;              // rounds a wave takes, waves a token
+  int rounds_q, rounds_k;  // waves over a token's query heads, key (and value) heads
 };
 
 struct RopeBwdParams {

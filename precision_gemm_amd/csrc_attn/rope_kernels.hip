@@ -12,7 +12,9 @@
 // it rotates, so the rotation needs no exchange between lanes, whichever way the pairs are
 // laid out and however much of the head is rotated; only the norm's sums cross lanes
 // (log2(D / 16) butterfly steps).  The 64 / (D / 16) heads of a wave's round are neighbours,
-// so its loads and stores run over whole cache lines.
+// so its loads and stores run over whole cache lines.  Results are stored the ordinary way:
+// stores past the caches make these kernels faster alone (4,096 tokens, backward: 33.9 to 29.3 us)
+// and whoever reads the results slower by more (with a copy of them 48.8 to 52.2 us).
 #include <algorithm>
 
 #include "attn_kernels.hpp"
@@ -109,96 +111,85 @@ __device__ __forceinline__ uint32_t fp8x4(const float* v) {
 
 enum { FORWARD = 0, APPEND_BF16 = 1, APPEND_FP8 = 2 };
 
-// One wave takes `per_wave` rounds of a token: a round is 64 / LPH heads of one kind (queries,
-// keys or, for the append, values).  The loads of all its rounds are issued before the first
-// is used.
-template <int D, int MODE, int PW>
+// A wave takes one round of a token: 64 / LPH heads of one kind (queries, keys or, for the append,
+// values).  Waves this short hide each other's latencies; two, three and four rounds a wave, all
+// loads first, are slower up to 1,024 tokens (32 + 8 + 8 heads of 128, 16 tokens: 3.0 us, then 3.8,
+// 4.6 and 5.4) and no faster at 4,096 (21.7 us with inputs out of HBM, 4.0 TB/s; 22.6, 23.0, 23.9;
+// a copy of as many bytes 19.3).
+template <int D, int MODE>
 __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH;
   const int lane = threadIdx.x & 63;
   const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
-  const int t = item / p.groups;
+  const int rounds = p.rounds_q + p.rounds_k + (MODE == FORWARD ? 0 : p.rounds_k);
+  const int t = item / rounds, r = item - t * rounds;
   if (t >= p.T) return;
-  const int r0 = (item - t * p.groups) * PW;
-  const int rounds = p.rounds_q + p.rounds_k + (MODE == FORWARD ? 0 : p.rounds_v);
   const int sl = lane / LPH, j = lane % LPH;
   const LaneMap m = lane_map(j, p.rot, p.interleaved);
 
-  uint4 xa[PW], xb[PW];
-#pragma unroll
-  for (int i = 0; i < PW; ++i) {
-    const int r = r0 + i;
-    xa[i] = xb[i] = zero4();
-    if (r >= rounds) continue;
-    const int kind = r < p.rounds_q ? 0 : r < p.rounds_q + p.rounds_k ? 1 : 2;
-    const int h = (r - (kind == 0 ? 0 : kind == 1 ? p.rounds_q : p.rounds_q + p.rounds_k)) * SLOTS + sl;
-    if (h >= (kind == 0 ? p.n_q : p.n_kv)) continue;
+  const int kind = r < p.rounds_q ? 0 : r < p.rounds_q + p.rounds_k ? 1 : 2;
+  const int h = (r - (kind == 0 ? 0 : kind == 1 ? p.rounds_q : p.rounds_q + p.rounds_k)) * SLOTS + sl;
+  const bool live = h < (kind == 0 ? p.n_q : p.n_kv);
+  uint4 xa = zero4(), xb = zero4();
+  if (live) {
     const uint16_t* src = p.qkv + (long)t * p.ld + (long)(h + (kind == 0 ? 0 : kind == 1 ? p.n_q : p.n_q + p.n_kv)) * D;
-    xa[i] = ldg16(src + m.a);
-    xb[i] = ldg16(src + m.b);
+    xa = ldg16(src + m.a);
+    xb = ldg16(src + m.b);
   }
   int pos = p.rot ? p.positions[t] : 0;
   const bool placed = p.rot == 0 || (unsigned)pos < (unsigned)p.max_pos;
   if (!placed) {
     pos = 0;
-    if (p.status && lane == 0 && r0 == 0) or_agent(p.status, ST_POSITION);
+    if (p.status && lane == 0 && r == 0) or_agent(p.status, ST_POSITION);
   }
   int slot = 0;
   if (MODE != FORWARD) {
     slot = p.slots[t];
     if ((long)slot >= p.n_slots) {
       slot = -1;
-      if (p.status && lane == 0 && r0 == 0) or_agent(p.status, ST_SLOT);
+      if (p.status && lane == 0 && r == 0) or_agent(p.status, ST_SLOT);
     }
     if (!placed) slot = -1;
   }
   const Turn tn = load_turn(p.cos_sin, pos, p.rot, m);
 
+  float v[16];
+  widen(xa, v);
+  widen(xb, v + 8);
+  if (MODE == FORWARD || kind < 2) {
+    const float* w = kind == 0 ? p.q_weight : p.k_weight;
+    if (w) {
+      float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < PW; ++i) {
-    const int r = r0 + i;
-    if (r >= rounds) break;
-    const int kind = r < p.rounds_q ? 0 : r < p.rounds_q + p.rounds_k ? 1 : 2;
-    const int h = (r - (kind == 0 ? 0 : kind == 1 ? p.rounds_q : p.rounds_q + p.rounds_k)) * SLOTS + sl;
-    const bool live = h < (kind == 0 ? p.n_q : p.n_kv);
-    float v[16];
-    widen(xa[i], v);
-    widen(xb[i], v + 8);
-    if (MODE == FORWARD || kind < 2) {
-      const float* w = kind == 0 ? p.q_weight : p.k_weight;
-      if (w) {
-        float ss = 0.f;
+      for (int e = 0; e < 16; ++e) ss += v[e] * v[e];
+      const float rs = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / D) + p.eps);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss += v[e] * v[e];
-        const float rs = 1.0f / sqrtf(head_sum<LPH>(ss) * (1.0f / D) + p.eps);
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
-          v[4 * q4] *= rs * w4.x; v[4 * q4 + 1] *= rs * w4.y; v[4 * q4 + 2] *= rs * w4.z; v[4 * q4 + 3] *= rs * w4.w;
-        }
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
+        v[4 * q4] *= rs * w4.x; v[4 * q4 + 1] *= rs * w4.y; v[4 * q4 + 2] *= rs * w4.z; v[4 * q4 + 3] *= rs * w4.w;
       }
-      turn<1>(v, tn, p.interleaved, m.turns);
     }
-    if (!live) continue;
-    if (MODE == FORWARD || kind == 0) {
-      uint16_t* dst = kind == 0 ? p.q_out + (long)t * p.ldq + (long)h * D : p.k_out + (long)t * p.ldk + (long)h * D;
-      *reinterpret_cast<uint4*>(dst + m.a) = placed ? narrow(v) : zero4();
-      *reinterpret_cast<uint4*>(dst + m.b) = placed ? narrow(v + 8) : zero4();
-    } else if (slot >= 0) {
-      const int off = slot & ((1 << p.page_log2) - 1);
-      const long row = ((((long)(slot >> p.page_log2) * p.n_kv + h) << p.page_log2) + off) * D;
-      if (MODE == APPEND_BF16) {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(kind == 1 ? p.k_cache : p.v_cache) + row;
-        *reinterpret_cast<uint4*>(dst + m.a) = narrow(v);
-        *reinterpret_cast<uint4*>(dst + m.b) = narrow(v + 8);
-      } else {
-        uint8_t* dst = reinterpret_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache) + row;
-        const float inv = 1.0f / (kind == 1 ? p.k_scale : p.v_scale)[h];
+    turn<1>(v, tn, p.interleaved, m.turns);
+  }
+  if (!live) return;
+  if (MODE == FORWARD || kind == 0) {
+    uint16_t* dst = kind == 0 ? p.q_out + (long)t * p.ldq + (long)h * D : p.k_out + (long)t * p.ldk + (long)h * D;
+    *reinterpret_cast<uint4*>(dst + m.a) = placed ? narrow(v) : zero4();
+    *reinterpret_cast<uint4*>(dst + m.b) = placed ? narrow(v + 8) : zero4();
+  } else if (slot >= 0) {
+    const int off = slot & ((1 << p.page_log2) - 1);
+    const long row = ((((long)(slot >> p.page_log2) * p.n_kv + h) << p.page_log2) + off) * D;
+    if (MODE == APPEND_BF16) {
+      uint16_t* dst = reinterpret_cast<uint16_t*>(kind == 1 ? p.k_cache : p.v_cache) + row;
+      *reinterpret_cast<uint4*>(dst + m.a) = narrow(v);
+      *reinterpret_cast<uint4*>(dst + m.b) = narrow(v + 8);
+    } else {
+      uint8_t* dst = reinterpret_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache) + row;
+      const float inv = 1.0f / (kind == 1 ? p.k_scale : p.v_scale)[h];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] *= inv;
-        *reinterpret_cast<uint2*>(dst + m.a) = make_uint2(fp8x4(v), fp8x4(v + 4));
-        *reinterpret_cast<uint2*>(dst + m.b) = make_uint2(fp8x4(v + 8), fp8x4(v + 12));
-      }
+      for (int e = 0; e < 16; ++e) v[e] *= inv;
+      *reinterpret_cast<uint2*>(dst + m.a) = make_uint2(fp8x4(v), fp8x4(v + 4));
+      *reinterpret_cast<uint2*>(dst + m.b) = make_uint2(fp8x4(v + 8), fp8x4(v + 12));
     }
   }
 }
@@ -370,16 +361,8 @@ hipError_t launch_mode(RopeParams p, hipStream_t s) {
   constexpr int SLOTS = 64 / (D / 16);
   p.rounds_q = (p.n_q + SLOTS - 1) / SLOTS;
   p.rounds_k = (p.n_kv + SLOTS - 1) / SLOTS;
-  p.rounds_v = MODE == FORWARD ? 0 : p.rounds_k;
-  const int rounds = p.rounds_q + p.rounds_k + p.rounds_v;
-  const bool wide = (long)p.T * rounds >= 4096;
-  p.per_wave = wide ? 4 : 1;
-  p.groups = (rounds + p.per_wave - 1) / p.per_wave;
-  const dim3 grid((unsigned)(((long)p.T * p.groups + 3) / 4));
-  if (wide)
-    hipLaunchKernelGGL((k_norm_rope<D, MODE, 4>), grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_norm_rope<D, MODE, 1>), grid, dim3(256), 0, s, p);
+  const int rounds = p.rounds_q + p.rounds_k + (MODE == FORWARD ? 0 : p.rounds_k);
+  hipLaunchKernelGGL((k_norm_rope<D, MODE>), dim3((unsigned)(((long)p.T * rounds + 3) / 4)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
