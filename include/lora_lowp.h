@@ -433,7 +433,7 @@ lora_status lora_qk_norm_rope(const uint16_t* qkv, int64_t ld, const int32_t* po
 /* Gradients of lora_qk_norm_rope: from dq bf16 [T][n_q D] and dk bf16 [T][n_kv D] (dense) to
  * dqkv bf16 [T] rows (stride ldd) and, with weights, dq_weight and dk_weight float [D] (written,
  * not accumulated into; zero for T == 0).  With g the rotation by minus the position of dy and
- * xh = x / sqrt(mean(x^2) + eps):  dw_d = sum g_d xh_d,  dx = (g w - xh mean(g w xh)) xh / x.
+ * r = 1 / sqrt(mean(x^2) + eps), xh = r x:  dw_d = sum g_d xh_d,  dx = r (g w - xh mean(g w xh)).
  *  - dv bf16 [T][n_kv D] is copied to the value heads' places of dqkv; NULL: they are not
  *    written (a caller may have the attention's backward write them there);
  *  - qkv: the forward's input (NULL without weights: it is not read); it may not overlap dqkv;
@@ -468,7 +468,8 @@ lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* 
 /* Masks of drafted trees from their parents: parents int32 [T] (index of a token's parent
  * among its own sequence's drafted tokens, before its own; negative: the token follows the
  * cached prefix), q_indptr int32 [B + 1] as below -> mask uint64 [T][words], bit i % 64 of word
- * i / 64 set for the token itself and its ancestors.  max_q <= 64 words, words <= 16. */
+ * i / 64 set for the token itself and its ancestors.  max_q <= 64 words, words <= 16.  Rows of
+ * no sequence, and of one whose tokens do not fit (LORA_ATTN_BAD_LENGTH), are 0. */
 lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t B, int32_t T, int32_t max_q,
                            int32_t words, uint64_t* mask, int32_t* status, void* stream);
 
@@ -481,8 +482,8 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
  * (NULL), those up to itself (one token: plain decode; more: a chunk of a prompt).
  *  - q bf16 [T] rows of n_q D (stride ldq); query heads h n_q / n_kv .. share kv head h
  *    (n_q % n_kv == 0);
- *  - page_table int32 [B][max_pages] (max_pages * page_size <= 2^30), kv_len int32 [B], q_indptr int32 [B + 1] (ascending, from
- *    0 to T), max_q at least every n_b; B <= 4096;
+ *  - page_table int32 [B][max_pages] (max_pages * page_size <= 2^30), kv_len int32 [B],
+ *    q_indptr int32 [B + 1] (ascending, from 0 to T), max_q at least every n_b; B <= 4096;
  *  - tree_mask uint64 [T][mask_words], max_q <= 64 mask_words, mask_words <= 16;
  *  - out bf16 [T][n_q D]; lse float [T][n_q] or NULL: the natural logarithm of the sum of
  *    exponentials.  A row that sees nothing (or only scores of -inf) gets out 0, lse -inf;

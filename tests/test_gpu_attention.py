@@ -325,6 +325,31 @@ def test_tree_mask_bad_parent():
     assert status.item() == P.LORA_ATTN_BAD_PARENT and m == [[1], [2], [5], [8]]
 
 
+@pytest.mark.parametrize("ns", [[64] * 3, [1024, 1, 513], [65, 128, 2]])
+def test_tree_mask_chains(ns):
+    """The deepest trees: every token the child of the one before."""
+    import precision_gemm_amd as P
+    print("[case] tree_mask chains", ns, flush=True)
+    indptr = np.concatenate([[0], np.cumsum(ns)])
+    parents = np.concatenate([np.arange(n) - 1 for n in ns])
+    m = P.tree_mask(_i32(parents), _i32(indptr), max(ns)).cpu().numpy().view(np.uint64)
+    for row, j in zip(m, (j for n in ns for j in range(n))):
+        assert sum(int(w) << 64 * i for i, w in enumerate(row)) == (1 << (j + 1)) - 1
+
+
+@pytest.mark.parametrize("indptr,rows", [([2, 4], [0, 0, 1, 3]), ([0, 3], [1, 3, 7, 0]), ([0, 2, 9], [1, 3, 0, 0]),
+                                         ([-1, 2, 4], [0, 0, 1, 3]), ([0, 4], [0, 0, 0, 0])])
+def test_tree_mask_bad_lengths(indptr, rows):
+    """Rows that no sequence has, or whose sequence does not fit (more than max_q = 3 tokens), are 0."""
+    torch = _torch()
+    import precision_gemm_amd as P
+    print("[case] tree_mask bad lengths", indptr, flush=True)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    parents = [-1, 0, 1, 2] if indptr[0] == 0 and len(indptr) == 2 else [-1, 0, -1, 0]
+    m = P.tree_mask(_i32(parents), _i32(indptr), 3, status=status).cpu().flatten().tolist()
+    assert status.item() == P.LORA_ATTN_BAD_LENGTH and m == rows
+
+
 # ---- attention ----
 
 def _put(t, where, code8, value):
