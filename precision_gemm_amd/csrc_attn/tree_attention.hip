@@ -377,6 +377,10 @@ __device__ __forceinline__ void put_tile(const TreeAttnParams& p, int q0, int ro
   if (g == 0 && p.lse) p.lse[at] = L == 0.f ? NEG_INF : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
 }
 
+// Few rows: four waves split a step's 128 keys.  Bound by HBM: 64 sequences of up to 8,192 keys in
+// 16 bits, 4 rows a kv head (922 MB), 166 us, 5.5 TB/s; one of 131,072 in 8 bits 51 us, 5.3 TB/s.
+// Short work is bound by latencies: of the 16 us for 16 sequences of 1,024 keys (67 MB) the first
+// 4 pass before keys are on their way (the launch, the prefix sum, the page table, the queries).
 template <int D, int RT, bool FP8, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   using G = Geo<D, FP8>;
@@ -630,7 +634,10 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
 
 // Joins the pieces of a unit cut between workgroups: grid (workgroups, row groups).  The lanes
 // of a wave go over a row's values and, where those are fewer than 64 x 4, over the pieces; the
-// four waves take a row each, or with WIDE a row's pieces in turn.
+// four waves take a row each, or with WIDE a row's pieces in turn.  A chain of latencies, a launch's
+// among them: 4.0 us for 4 pieces a unit, 5.9 for the 64 pieces of one long sequence.  (Joining in
+// the workgroup that finishes a unit last needs its pieces written through to memory, and counters:
+// slower on every case that was measured.)
 template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int block_rows) {
   const int wg = blockIdx.x;
@@ -708,11 +715,18 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
 }
 
 // The same for many rows (trees of many tokens times a group of heads; a prompt's chunk): eight
-// waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128 rows, put into LDS as
-// MFMA operands (K and the transposed V in bf16, 1 KB a wave's read, conflict free; an 8-bit
-// cache is widened once, here), and each wave takes 16 rows through all of them; of 64 rows
-// or fewer, two or four waves share each 16 (32 sequences of 2,048 keys, 64 rows: 61 us against
-// 70).  The next round's loads are in flight, in registers, while one is computed.
+// waves share the keys, in rounds of up to four groups of 32.  They are loaded once for up to 128
+// rows, put into LDS as MFMA operands (K and the transposed V in bf16, 1 KB a wave's read, conflict
+// free; an 8-bit cache is widened once, here), and each wave takes 16 rows through all of them; of
+// 64 rows or fewer, two or four waves share each 16 (32 sequences of 2,048 keys, 64 rows: 61 us
+// against 70).  The next round's loads are in flight, in registers, while one is computed.
+// Bound by LDS: 16 sequences with trees of 64 tokens over up to 2,048 keys (128 rows a workgroup,
+// 8-bit cache) take 45 us, 207 TFLOP/s; a round of 128 keys spends 4,300 cycles in its four groups
+// (eight waves read 16 KB of operands each a group, 1,024 cycles at 128 B a cycle), 700 in putting
+// the next into LDS and 2,300 at barriers.  Two sets of operands in LDS, one barrier a round: 4 %
+// faster with 8-bit caches, 10 % slower with 16-bit ones.  Half the reads, by two row tiles a wave
+// in workgroups of four waves, two a CU: 13 % faster for 32 such sequences, 13 to 55 % slower for
+// 16 and fewer, which are then cut into twice the pieces.
 // A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
 // of O^T, so that its stores and the join's loads are whole KBs and a wave of the join, which
 // takes one x, has neighbouring values of a row.
@@ -993,7 +1007,8 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
 // Joins the pieces of k_tree_attention_rows: a workgroup a row tile, a wave one x of it.  The
 // pieces are taken KR at a time with a running maximum, so that all loads of a round, the
 // pieces' (m, l) among them, are in flight together: the launch is a chain of latencies (a
-// pass of its own over the maxima, and a wave for a whole tile, took 10.8 us at 64 rows).
+// pass of its own over the maxima, and a wave for a whole tile, took 10.8 us at 64 rows; this 6.3,
+// and 10.0 for 256 units of 128 rows, whose pieces are 22 MB written and read).
 template <int D, int CH>
 __global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int block_rows) {
   constexpr int NV = D / 64, KR = D == 256 ? 4 : 8;  // float4 of a lane; pieces of a round
@@ -1150,7 +1165,7 @@ TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   } else {
     pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;
     pl.block_rows = 16 * pl.row_tiles;
-    pl.n_wg = pl.row_tiles == 1 && D <= 128 ? 512 : 256;
+    pl.n_wg = pl.row_tiles == 1 && D <= 128 ? 512 : 256;  // what the registers let run at once: two a CU, or one
   }
   const size_t slots = 2 * (size_t)pl.n_wg, r = (size_t)pl.block_rows;
   pl.desc_bytes = (size_t)pl.n_wg * ATTN_DESC * 4;
