@@ -889,7 +889,6 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     float m[1] = {NEG_INF}, l[1] = {0.f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[0][t] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (tid < 64) smask[tid] = mask_row;  // read after the rounds' barriers
 
     // 32 keys; SPECIAL where they reach the drafted ones, the end or a page that does not exist
     auto group = [&](auto special_t, int gr, int key0, uint32_t bad) {
@@ -941,7 +940,8 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     };
 
     for (int t = g0; t < g1; t += GR) {
-      __syncthreads();  // the round before is read
+      __syncthreads();  // the round before is read, and its masks, which may be another sequence's
+      if (t == g0 && tid < 64) smask[tid] = mask_row;
       stage(t);
       if (t + GR < g1) fetch(t + GR);
       __syncthreads();

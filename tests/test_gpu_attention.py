@@ -453,6 +453,8 @@ ATTN = [  # ns, kvs, n_q, n_kv, D, page, mask
     ([1], [40000], 16, 2, 128, 1024, "none"),
     ([2, 1], [90000, 70], 8, 1, 64, 16, "none"),
     ([1] * 300, [1 + (37 * b) % 90 for b in range(300)], 2, 1, 64, 16, "none"),
+    # more units than workgroups, of 80 to 132 rows each: a workgroup goes from tree to tree
+    ([20 + b % 14 for b in range(48)], [60 + 29 * b % 190 for b in range(48)], 32, 8, 128, 16, "tree"),
 ]
 
 
