@@ -868,8 +868,9 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     if (p.mask && p.words == 1 && tid < sq.n) mask_row = p.mask[sq.q0 + tid];
     if (g0 < g1) fetch(g0);
 
-    // scores in log2 units; a negative scale is taken as the queries' sign
-    const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = fabsf(scale);
+    // scores in log2 units; a negative scale is taken as the queries' sign, a scale of 0 as queries
+    // of 0 (the -inf of a key that is not seen stays -inf)
+    const float scale = FP8 ? p.scale_log2 * p.k_scale[h] : p.scale_log2, sc = scale == 0.f ? 1.f : fabsf(scale);
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
     // Eight row tiles of 16, a wave each; of four or fewer (two or fewer), two (four) waves take
     // each, with the groups of a round between them.
@@ -883,16 +884,15 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       const int r = row0 + i, j = r / p.group;
       const uint16_t* src = p.q + (long)(sq.q0 + min(j, sq.n - 1)) * p.ldq + (long)(h * p.group + (r - j * p.group)) * D;
 #pragma unroll
-      for (int s = 0; s < G::KS; ++s) q[s] = r < rows ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
+      for (int s = 0; s < G::KS; ++s) q[s] = r < rows && scale != 0.f ? signed_q(ldg16(src + q_place<FP8>(s, g)), flip) : zero4();
     }
     v4f o[1][NT];
     float m[1] = {NEG_INF}, l[1] = {0.f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[0][t] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    // 32 keys; SPECIAL where they reach the drafted ones, the end or a page that does not exist
-    auto group = [&](auto special_t, int gr, int key0, uint32_t bad) {
-      constexpr bool SPECIAL = decltype(special_t)::value;
+    // 32 keys; `special` where they reach the drafted ones, the end or a page that does not exist
+    auto group = [&](bool special, int gr, int key0, uint32_t bad) {
       // operands come from LDS a window ahead of the products (left alone, the compiler reads
       // one, waits, and multiplies: 16-token trees 18.0 us against 17.0)
       // (heads of 256 have no registers for it: one at a time, in pairs of products)
@@ -914,9 +914,12 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       }
       uint4 pb[1];
       uint32_t vis[1] = {0};
-      if constexpr (SPECIAL)
+      if (special) {
         vis[0] = (bad >> (g >> 1)) & 1u ? 0u : visible8(p, smask, sq.q0, min((row0 + i) / p.group, sq.n - 1), key0 + 8 * g - prefix, sq.n);
-      softmax_step<NT, 1, SPECIAL>(s, sc, vis, m, l, o, pb);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0][e >> 2][e & 3] = (vis[0] >> e) & 1u ? s[0][e >> 2][e & 3] : NEG_INF;
+      }
+      softmax_step<NT, 1, false>(s, sc, vis, m, l, o, pb);
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt) {
         o[0][tt] = mfma_bf16_16x16x32(AHEAD ? win[(KN + tt) % WIN] : sv(gr, tt), pb[0], o[0][tt]);
@@ -924,7 +927,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
           if (tt + WIN < NT) win[(KN + tt) % WIN] = sv(gr, tt + WIN);
         if (AHEAD || (tt & 1)) __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (SPECIAL) {
+      if (special) {
 #pragma unroll
         for (int part = 0; part < PARTS / 2; ++part) {
           const uint32_t odd = __builtin_amdgcn_readfirstlane((int)s_odd[gr][part]);
@@ -948,10 +951,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
       for (int gr = mine_of; gr < GR && t + gr < g1 && busy; gr += split) {
         const int key0 = (t + gr) * ATTN_GROUP;
         const uint32_t bad = __builtin_amdgcn_readfirstlane((int)s_bad[gr]);
-        if (key0 + 32 > prefix || bad)
-          group(std::true_type{}, gr, key0, bad);
-        else
-          group(std::false_type{}, gr, key0, 0);
+        group(key0 + 32 > prefix || bad, gr, key0, bad);
       }
     }
 
@@ -1154,10 +1154,10 @@ hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t
 
 TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   TreeAttnPlan pl;
-  // 17 to 32 rows of an 8-bit cache: waves that split the keys, with two tiles of rows, do not
-  // put what they widen through LDS (32 sequences of 2,048 keys, 32 rows: 40 us against 48; in
-  // 16 bits 58 against 55)
-  pl.shared = rows > (fp8 && D <= 128 ? 32 : 16);
+  // 17 to 32 rows of an 8-bit cache: waves that split the keys, with two tiles of rows (heads of
+  // 256: two blocks), do not put what they widen through LDS (32 sequences of 2,048 keys, 32 rows:
+  // 40 us against 48, heads of 256 99 against 112; in 16 bits 58 against 55 and 189 against 108)
+  pl.shared = rows > (fp8 ? 32 : 16);
   if (pl.shared) {
     pl.row_tiles = 1;
     pl.block_rows = 16 * ROW_WAVES;
