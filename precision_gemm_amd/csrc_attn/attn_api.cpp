@@ -59,6 +59,8 @@ RopeParams rope_params(const uint16_t* qkv, int64_t ld, const int32_t* positions
   return p;
 }
 
+inline int plan_rows(int64_t rows) { return rows > 65536 ? 65536 : (int)rows; }
+
 inline size_t plan_bytes(const TreeAttnPlan& pl) {
   return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
 }
@@ -161,9 +163,9 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
 size_t lora_tree_attention_workspace_bytes(int32_t n_q, int32_t n_kv, int32_t D, int32_t max_q) {
   if (check_heads(1, n_q, n_kv, D) != LORA_OK || n_q % n_kv != 0 || max_q < 1 || max_q > MAX_TOKENS) return 0;
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
-  size_t most = 0;  // of the two cache formats
-  for (int fp8 = 0; fp8 < 2; ++fp8) {
-    const size_t n = plan_bytes(tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows, fp8));
+  size_t most = 0;  // of the two cache formats, few sequences and many
+  for (int way = 0; way < 4; ++way) {
+    const size_t n = plan_bytes(tree_attn_plan(D, plan_rows(rows), way & 1, way & 2 ? (long)ATTN_MAX_B * n_kv : 1));
     most = n > most ? n : most;
   }
   return most;
@@ -196,12 +198,12 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))) return LORA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
   if (rows > INT32_MAX / 2) return LORA_ERR_UNSUPPORTED;
-  const TreeAttnPlan pl = tree_attn_plan(D, rows > 65536 ? 65536 : (int)rows, fp8);
+  const TreeAttnPlan pl = tree_attn_plan(D, plan_rows(rows), fp8, (long)B * n_kv);
   // all steps of a call are numbered in 32 bits
   const double steps = (double)B * n_kv * (double)((rows + pl.block_rows - 1) / pl.block_rows) *
                        ((double)max_pages * page_size / ATTN_KEYS + 1.0);
   if (steps > 2.0e9) return LORA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < plan_bytes(pl))
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_tree_attention_workspace_bytes(n_q, n_kv, D, max_q))
     return LORA_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
   TreeAttnParams p{};

@@ -729,18 +729,20 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
 // faster with 8-bit caches, 10 % slower with 16-bit ones.  Half the reads, by two row tiles a wave
 // in workgroups of four waves, two a CU: 13 % faster for 32 such sequences, 13 to 55 % slower for
 // 16 and fewer, which are then cut into twice the pieces.
+// WGS: workgroups a CU. Two, where there are units enough for twice the workgroups, fill each
+// other's waits (figures at tree_attn_plan).
 // A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
 // of O^T, so that its stores and the join's loads are whole KBs and a wave of the join, which
 // takes one x, has neighbouring values of a row.
 constexpr int ROW_WAVES = 8;
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeAttnParams p) {
+template <int D, bool FP8, int WGS>
+__global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows(TreeAttnParams p) {
   using G = Geo<D, FP8>;
   constexpr int NT = D / 16, BLOCK = 16 * ROW_WAVES;
   // a round's groups of 32 keys, the waves that load one, and a wave's words of a key: half a
-  // group's K or V (heads of 256: a quarter), 8 to 32 registers
-  constexpr int GR = D == 256 ? 2 : 4, PARTS = ROW_WAVES / GR, SW = G::NCH * G::VW / (PARTS / 2);
+  // group's K or V (heads of 256, and of 128 with two workgroups a CU: a quarter), 8 to 32 registers
+  constexpr int GR = D * WGS >= 256 ? 2 : 4, PARTS = ROW_WAVES / GR, SW = G::NCH * G::VW / (PARTS / 2);
   static_assert(2 * G::KL / (PARTS / 2) == 2 * SW, "keys and values take the same registers");
   // V in parts: by a lane's loads of a key, or within its one load
   constexpr int LOADS = PARTS == 2 ? G::NCH : 1, LOAD_BYTES = 4 * SW / LOADS;
@@ -897,9 +899,9 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2) void k_tree_attention_rows(TreeA
     auto group = [&](bool special, int gr, int key0, uint32_t bad) {
       // operands come from LDS a window ahead of the products (left alone, the compiler reads
       // one, waits, and multiplies: 16-token trees 18.0 us against 17.0)
-      // (heads of 256 have no registers for it: one at a time, in pairs of products)
+      // (where registers are short, one at a time, in pairs of products)
       constexpr int WIN = 4, KN = 2 * G::KS;
-      constexpr bool AHEAD = D <= 128;
+      constexpr bool AHEAD = D * WGS < 256;
       uint4 win[AHEAD ? WIN : 1];
       auto k_at = [&](int n) { return sk(gr, n & 1, n >> 1); };
       v4f s[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
@@ -1133,10 +1135,10 @@ void launch_few(const TreeAttnParams& p, hipStream_t s) {
     hipLaunchKernelGGL((k_tree_combine<D, false>), dim3(p.n_wg, (rows + 3) / 4), dim3(256), 0, s, p, RT * 16);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int WGS>
 void launch_rows(const TreeAttnParams& p, hipStream_t s) {
   constexpr int BLOCK = 16 * ROW_WAVES;
-  hipLaunchKernelGGL((k_tree_attention_rows<D, FP8>), dim3(p.n_wg), dim3(64 * ROW_WAVES), (p.B + 1) * sizeof(int), s, p);
+  hipLaunchKernelGGL((k_tree_attention_rows<D, FP8, WGS>), dim3(p.n_wg), dim3(64 * ROW_WAVES), (p.B + 1) * sizeof(int), s, p);
   const long rows = min((long)BLOCK, (long)p.max_q * p.group);
   hipLaunchKernelGGL((k_tree_combine_rows<D, Geo<D, FP8>::CH>), dim3(p.n_wg, (unsigned)((rows + 15) / 16)), dim3(256), 0, s, p, BLOCK);
 }
@@ -1144,7 +1146,12 @@ void launch_rows(const TreeAttnParams& p, hipStream_t s) {
 template <int D, bool FP8>
 hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t s) {
   if (pl.shared) {
-    launch_rows<D, FP8>(p, s);
+    if constexpr (D <= 128) {
+      if (pl.n_wg > 256) launch_rows<D, FP8, 2>(p, s);
+      else launch_rows<D, FP8, 1>(p, s);
+    } else {
+      launch_rows<D, FP8, 1>(p, s);
+    }
   } else {
     if (pl.row_tiles == 1) launch_few<D, 1, FP8>(p, s);
     else if constexpr (D <= 128 && FP8) launch_few<D, 2, FP8>(p, s);
@@ -1154,7 +1161,7 @@ hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t
 
 }  // namespace
 
-TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
+TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8, long heads) {
   TreeAttnPlan pl;
   // 17 to 32 rows of an 8-bit cache: waves that split the keys, with two tiles of rows (heads of
   // 256: two blocks), do not put what they widen through LDS (32 sequences of 2,048 keys, 32 rows:
@@ -1163,7 +1170,13 @@ TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8) {
   if (pl.shared) {
     pl.row_tiles = 1;
     pl.block_rows = 16 * ROW_WAVES;
-    pl.n_wg = 256;
+    const long units = heads * ((rows + pl.block_rows - 1) / pl.block_rows);
+    // two workgroups a CU from 512 units on (heads of 64: 384), where they are not cut into twice
+    // the pieces. Sequences of 2,048 keys, 8 kv heads, one and two a CU, in us: heads of 128, 8-bit
+    // cache, 64 sequences of 64 rows 108 and 91, 32 of 256 rows 130 and 115, 48 of 64 (384 units)
+    // 88 and 85; 16-bit 64 of 128 rows 147 and 133, 48 of 64 95 and 105; heads of 64, 64 of 64
+    // rows 73 and 50, 48 of 64 55 and 47, 32 of 128 (256 units) 46 and 53
+    pl.n_wg = D <= 128 && units >= (D == 64 ? 384 : 512) ? 512 : 256;
   } else {
     pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;
     pl.block_rows = 16 * pl.row_tiles;

@@ -455,6 +455,8 @@ ATTN = [  # ns, kvs, n_q, n_kv, D, page, mask
     ([1] * 300, [1 + (37 * b) % 90 for b in range(300)], 2, 1, 64, 16, "none"),
     # more units than workgroups, of 80 to 132 rows each: a workgroup goes from tree to tree
     ([20 + b % 14 for b in range(48)], [60 + 29 * b % 190 for b in range(48)], 32, 8, 128, 16, "tree"),
+    ([9 + b % 6 for b in range(50)], [15 + 53 * b % 400 for b in range(50)], 32, 8, 64, 32, "any"),
+    ([33, 32], [33, 300], 128, 64, 64, 16, "none"),
 ]
 
 
@@ -472,7 +474,7 @@ def test_attention_ignores_what_is_not_seen(fp8):
     that a row does not see; rows that do see one get it."""
     torch = _torch()
     print("[case] NaN in keys that are not seen", fp8, flush=True)
-    for D, n_q, n_kv in ((128, 4, 2), (64, 20, 2), (256, 3, 1)):
+    for D, n_q, n_kv in ((128, 4, 2), (64, 20, 2), (256, 3, 1), (128, 1024, 256), (64, 1024, 256)):
         b = Batch(9, [6, 9], [133, 40], n_q, n_kv, D, 16, fp8, "any")
         clean = b.run()
         b.check(*clean)
