@@ -735,13 +735,13 @@ __global__ __launch_bounds__(256) void k_tree_combine(TreeAttnParams p, int bloc
 // free; an 8-bit cache is widened once, here), and each wave takes 16 rows through all of them; of
 // 64 rows or fewer, two or four waves share each 16 (32 sequences of 2,048 keys, 64 rows: 61 us
 // against 70).  The next round's loads are in flight, in registers, while one is computed.
-// Bound by LDS: 16 sequences with trees of 64 tokens over up to 2,048 keys (128 rows a workgroup,
-// 8-bit cache) take 45 us, 207 TFLOP/s; a round of 128 keys spends 4,300 cycles in its four groups
-// (eight waves read 16 KB of operands each a group, 1,024 cycles at 128 B a cycle), 700 in putting
-// the next into LDS and 2,300 at barriers.  Two sets of operands in LDS, one barrier a round: 4 %
-// faster with 8-bit caches, 10 % slower with 16-bit ones.  Half the reads, by two row tiles a wave
-// in workgroups of four waves, two a CU: 13 % faster for 32 such sequences, 13 to 55 % slower for
-// 16 and fewer, which are then cut into twice the pieces.
+// 16 sequences with trees of up to 64 tokens over up to 2,048 keys, 8-bit cache: 36 us, 257 TFLOP/s.
+// Bound by the SIMDs' instructions and waits: a round of 128 keys spends 3,650 cycles in its four
+// groups (a wave's group is 256 cycles of products and about 300 of softmax, two waves a SIMD; its
+// operands are 1,024 cycles of LDS reads for the eight waves), 720 in putting the next round into
+// LDS and 1,900 at barriers.  Two row tiles a wave, with half the LDS reads, take as long: 2 to 4 %
+// less at 32 sequences of 256 rows, 2 us more wherever units are cut, for joining the waves.  Two
+// sets of operands in LDS, one barrier a round: 4 % less with 8-bit caches, 10 % more with 16-bit.
 // WGS: workgroups a CU. Two, where there are units enough for twice the workgroups, fill each
 // other's waits (figures at tree_attn_plan).
 // A piece's slot holds O in the lanes' own layout, [row tile][x = 0 .. 3][NT / 4][lane] x 4 tiles
@@ -1032,7 +1032,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
 // pieces are taken KR at a time with a running maximum, so that all loads of a round, the
 // pieces' (m, l) among them, are in flight together: the launch is a chain of latencies (a
 // pass of its own over the maxima, and a wave for a whole tile, took 10.8 us at 64 rows; this 6.3,
-// and 10.0 for 256 units of 128 rows, whose pieces are 22 MB written and read).
+// and 9.3 for 248 units of up to 128 rows, whose pieces are 20 MB written and read).
 template <int D, int CH>
 __global__ __launch_bounds__(256) void k_tree_combine_rows(TreeAttnParams p, int block_rows) {
   constexpr int NV = D / 64, KR = D == 256 ? 4 : 8;  // float4 of a lane; pieces of a round
