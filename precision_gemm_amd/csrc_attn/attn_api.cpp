@@ -59,8 +59,6 @@ RopeParams rope_params(const uint16_t* qkv, int64_t ld, const int32_t* positions
   return p;
 }
 
-inline int plan_rows(int64_t rows) { return rows > 65536 ? 65536 : (int)rows; }
-
 inline size_t plan_bytes(const TreeAttnPlan& pl) {
   return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
 }
@@ -162,10 +160,9 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
 
 size_t lora_tree_attention_workspace_bytes(int32_t n_q, int32_t n_kv, int32_t D, int32_t max_q) {
   if (check_heads(1, n_q, n_kv, D) != LORA_OK || n_q % n_kv != 0 || max_q < 1 || max_q > MAX_TOKENS) return 0;
-  const int64_t rows = (int64_t)max_q * (n_q / n_kv);
   size_t most = 0;  // of the two cache formats, few sequences and many
   for (int way = 0; way < 4; ++way) {
-    const size_t n = plan_bytes(tree_attn_plan(D, plan_rows(rows), way & 1, way & 2 ? (long)ATTN_MAX_B * n_kv : 1));
+    const size_t n = plan_bytes(tree_attn_plan(D, max_q, n_q / n_kv, way & 1, false, way & 2 ? (long)ATTN_MAX_B * n_kv : 1));
     most = n > most ? n : most;
   }
   return most;
@@ -198,7 +195,7 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))) return LORA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
   if (rows > INT32_MAX / 2) return LORA_ERR_UNSUPPORTED;
-  const TreeAttnPlan pl = tree_attn_plan(D, plan_rows(rows), fp8, (long)B * n_kv);
+  const TreeAttnPlan pl = tree_attn_plan(D, max_q, n_q / n_kv, fp8, tree_mask != nullptr, (long)B * n_kv);
   // all steps of a call, which count 3 at most, are numbered in 32 bits
   const double steps = (double)B * n_kv * (double)((rows + pl.block_rows - 1) / pl.block_rows) *
                        ((double)max_pages * page_size / ATTN_KEYS + 1.0);
@@ -213,7 +210,7 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   p.kv_len = kv_len; p.q_indptr = q_indptr; p.B = B; p.T = T; p.max_q = max_q; p.n_q = n_q; p.n_kv = n_kv;
   p.group = n_q / n_kv; p.mask = tree_mask; p.words = tree_mask ? mask_words : 0;
   p.scale_log2 = scale * 1.44269504088896341f;
-  p.out = out; p.lse = lse; p.status = status; p.n_wg = pl.n_wg;
+  p.out = out; p.lse = lse; p.status = status; p.n_wg = pl.n_wg; p.counted = pl.counted;
   p.desc = reinterpret_cast<int*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + round256(pl.desc_bytes));
   p.part_o = reinterpret_cast<float*>(ws + round256(pl.desc_bytes) + round256(pl.ml_bytes));

@@ -76,6 +76,7 @@ struct TreeAttnParams {
   float* part_ml;          // [2 n_wg][rows][2]
   float* part_o;           // [2 n_wg][rows][D]
   int n_wg;
+  int counted;             // a row block counts the steps that its tokens see, not all
   int* status;
 };
 
@@ -86,9 +87,10 @@ constexpr int ATTN_KEYS = 128;       // keys of a step: a group for each of four
 
 // How a call's rows (drafted tokens times query heads of a kv head) are taken: by waves that
 // split a step's keys, or (`shared`) that share them; row tiles of 16 a wave holds, rows of a
-// workgroup, workgroups.  `heads`: kv heads of all the call's sequences.
-struct TreeAttnPlan { bool shared; int row_tiles, block_rows, n_wg; size_t desc_bytes, ml_bytes, o_bytes; };
-TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8, long heads);
+// workgroup, workgroups; whether in-order row blocks are `counted` by what they see.  `heads`: kv
+// heads of all the call's sequences.
+struct TreeAttnPlan { bool shared, counted; int row_tiles, block_rows, n_wg; size_t desc_bytes, ml_bytes, o_bytes; };
+TreeAttnPlan tree_attn_plan(int D, int max_q, int group, bool fp8, bool mask, long heads);
 hipError_t launch_tree_attention(const TreeAttnParams& p, const TreeAttnPlan& pl, int D, bool fp8, hipStream_t s);
 hipError_t launch_tree_mask(const int* parents, const int* q_indptr, int B, int T, int max_q, int words, uint64_t* mask,
                             int* status, hipStream_t s);

@@ -123,6 +123,26 @@ __device__ __forceinline__ int step_weight(int rows) { return !SHARED ? 1 : rows
 // One sequence: its queries and keys, its steps, row blocks (the last one's steps count `last`),
 // and what the steps of one kv head's units count together.
 struct Seq { int q0, n, kv, steps, blocks, last, head, bad; };
+// Steps of row block rb of 128 rows, and of the blocks before it.  In order, `group` blocks hold 128
+// tokens, so that every `group` blocks a block's last token sees a step more.
+__device__ __forceinline__ bool in_order(const TreeAttnParams& p, const Seq& s) { return p.counted && s.kv >= s.n; }
+__device__ __forceinline__ int first_steps(const Seq& s) { return (s.kv - s.n + ATTN_KEYS - 1) / ATTN_KEYS + 1; }
+__device__ __forceinline__ int steps_of(const TreeAttnParams& p, const Seq& s, int rb) {
+  return in_order(p, s) ? min(s.steps, first_steps(s) + rb / p.group) : s.steps;
+}
+__device__ __forceinline__ int steps_before(const TreeAttnParams& p, const Seq& s, int rb) {
+  if (!in_order(p, s)) return rb * s.steps;
+  const int first = first_steps(s), m = rb / p.group;
+  return p.group * (m * first + m * (m - 1) / 2) + (rb - m * p.group) * min(s.steps, first + m);
+}
+// The row block that step x of a kv head's blocks is in.
+__device__ __forceinline__ int block_at(const TreeAttnParams& p, const Seq& s, int x) {
+  if (!in_order(p, s)) return x / s.steps;
+  int m = 0;
+  while ((m + 1) * p.group < s.blocks && steps_before(p, s, (m + 1) * p.group) <= x) ++m;
+  return m * p.group + (x - steps_before(p, s, m * p.group)) / steps_of(p, s, m * p.group);
+}
+
 template <bool SHARED>
 __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1, int kv, int block_rows) {
   Seq s;
@@ -135,7 +155,10 @@ __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1,
   s.steps = max(1, (s.kv + ATTN_KEYS - 1) / ATTN_KEYS);
   s.blocks = (s.n * p.group + block_rows - 1) / block_rows;
   s.last = step_weight<SHARED>(s.n * p.group - (s.blocks - 1) * block_rows);
-  s.head = s.blocks == 0 ? 0 : s.steps * ((s.blocks - 1) * (SHARED ? FULL : 1) + s.last);
+  const int full = s.blocks - 1;
+  if (s.blocks == 0) s.head = 0;
+  else if (SHARED) s.head = FULL * steps_before(p, s, full) + s.last * steps_of(p, s, full);
+  else s.head = s.steps * s.blocks;
   return s;
 }
 
@@ -783,7 +806,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
   const Stretch mine = find_stretch<64 * ROW_WAVES, true>(p, wg, BLOCK, cum, wave_sum, &found);
   if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
   int cur = mine.cur, b = mine.b;
-  Seq sq = mine.first;
+  int q0 = mine.first.q0, q1 = q0 + mine.first.n, kv_len = mine.first.kv;
   const int end = mine.end;
 
   const int page = 1 << p.page_log2;
@@ -794,18 +817,25 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
 
   while (cur < end) {
     while (__builtin_amdgcn_readfirstlane(cum[b + 1]) <= cur) ++b;
-    if (b != mine.b) sq = make_seq<true>(p, ld_table(p.q_indptr + b), ld_table(p.q_indptr + b + 1), ld_table(p.kv_len + b), BLOCK);
+    if (b != mine.b) {
+      q0 = ld_table(p.q_indptr + b);
+      q1 = ld_table(p.q_indptr + b + 1);
+      kv_len = ld_table(p.kv_len + b);
+    }
+    const Seq sq = make_seq<true>(p, q0, q1, kv_len, BLOCK);
     const int local = cur - __builtin_amdgcn_readfirstlane(cum[b]);
     const int h = local / sq.head, in_head = local - h * sq.head;
-    const int rb = min(in_head / (FULL * sq.steps), sq.blocks - 1), weight = rb == sq.blocks - 1 ? sq.last : FULL;
+    const int rb = min(block_at(p, sq, in_head / FULL), sq.blocks - 1), weight = rb == sq.blocks - 1 ? sq.last : FULL;
     // the unit's steps that begin in this stretch (of one cut inside its last step, none)
-    const int in_unit = in_head - rb * FULL * sq.steps, taken = min(weight * sq.steps - in_unit, end - cur);
+    const int steps = steps_of(p, sq, rb);
+    const int in_unit = in_head - FULL * steps_before(p, sq, rb), taken = min(weight * steps - in_unit, end - cur);
     auto begun = [&](int at) { return weight == FULL ? (at + FULL - 1) / FULL : (at + HALF_FULL - 1) / HALF_FULL; };
-    const int t0 = begun(in_unit), t1 = min(sq.steps, begun(in_unit + taken));
-    if (t0 == sq.steps) {
-      cur += taken;
-      continue;
-    }
+    const int t0 = begun(in_unit), t1 = min(steps, begun(in_unit + taken));
+    const bool whole = t0 == 0 && t1 == steps;
+    const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
+    if (!whole && t0 == 0 && tid == 0) put_desc(p, wg, (cur + (steps - 1) * weight) / mine.per - wg + 1, sq, h, rb);
+    cur += taken;
+    if (t0 == steps) continue;
     constexpr int PER_STEP = ATTN_KEYS / ATTN_GROUP;
     const int rows = sq.n * p.group, prefix = sq.kv - sq.n;
     // without a mask no row of this block sees past its last token
@@ -979,8 +1009,6 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
       }
     }
 
-    const bool whole = t0 == 0 && t1 == sq.steps;
-    const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
     l[0] += __shfl_xor(l[0], 16);
     l[0] += __shfl_xor(l[0], 32);
     if (split > 1) {  // join the waves of a tile, in order, in the first of them
@@ -1021,10 +1049,6 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
         if (g == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * ((long)slot * BLOCK + tile * 16 + i)) = make_float2(m[0], l[0]);
       }
     }
-    if (!whole && t0 == 0 && tid == 0) {
-      put_desc(p, wg, (cur + (sq.steps - 1) * weight) / mine.per - wg + 1, sq, h, rb);
-    }
-    cur += taken;
   }
 }
 
@@ -1181,8 +1205,10 @@ hipError_t launch_d(const TreeAttnParams& p, const TreeAttnPlan& pl, hipStream_t
 
 }  // namespace
 
-TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8, long heads) {
+TreeAttnPlan tree_attn_plan(int D, int max_q, int group, bool fp8, bool mask, long heads) {
+  const long rows = (long)max_q * group;
   TreeAttnPlan pl;
+  pl.counted = false;
   // 17 to 32 rows of an 8-bit cache: waves that split the keys, with two tiles of rows (heads of
   // 256: two blocks), do not put what they widen through LDS (32 sequences of 2,048 keys, 32 rows:
   // 40 us against 48, heads of 256 99 against 112; in 16 bits 58 against 55 and 189 against 108)
@@ -1197,6 +1223,13 @@ TreeAttnPlan tree_attn_plan(int D, int rows, bool fp8, long heads) {
     // 88 and 85; 16-bit 64 of 128 rows 147 and 133, 48 of 64 95 and 105; heads of 64, 64 of 64
     // rows 73 and 50, 48 of 64 55 and 47, 32 of 128 (256 units) 46 and 53
     pl.n_wg = D <= 128 && units >= (D == 64 ? 384 : 512) ? 512 : 256;
+    // A prompt's row blocks count what they see (32 + 8 + 8 heads of 128, in us, all alike and so:
+    // prompts of 1,024 tokens, 4 of them, 147 and 120, of 4,096 465 and 304, of 700, 4, 96 and 75, of
+    // 256, 32, 83 and 71; 800 more tokens of 8,000 178 and 170).  Not where all alike gives almost
+    // every workgroup a unit of its own and cuts none (8 prompts of 256 30 and 43, 512 more tokens of
+    // 2,048, 4, 113 and 126), unless the prompts are long (2,048: 126 and 110).
+    const bool own = units <= pl.n_wg && 8 * units > 7 * pl.n_wg && max_q < 1024;
+    pl.counted = !mask && rows > pl.block_rows && !own;
   } else {
     pl.row_tiles = rows <= 16 || D > 128 ? 1 : 2;
     pl.block_rows = 16 * pl.row_tiles;

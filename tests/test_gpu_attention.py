@@ -457,6 +457,11 @@ ATTN = [  # ns, kvs, n_q, n_kv, D, page, mask
     ([20 + b % 14 for b in range(48)], [60 + 29 * b % 190 for b in range(48)], 32, 8, 128, 16, "tree"),
     ([9 + b % 6 for b in range(50)], [15 + 53 * b % 400 for b in range(50)], 32, 8, 64, 32, "any"),
     ([33, 32], [33, 300], 128, 64, 64, 16, "none"),
+    # prompts and chunks of many row blocks, which see more and more keys
+    ([700, 130], [700, 900], 8, 2, 64, 64, "none"),
+    ([400, 0, 129, 1], [400, 30, 731, 300], 14, 2, 128, 16, "none"),
+    ([517], [1200], 1, 1, 256, 32, "none"),
+    ([150, 260], [150, 300], 24, 1, 128, 128, "none"),
 ]
 
 
@@ -576,6 +581,23 @@ def test_attention_data_errors():
         for s, (lo, hi) in enumerate(zip(keep[:-1], keep[1:])):
             if indptr[s] == lo and indptr[s + 1] == hi:
                 assert torch.equal(out[lo:hi], clean[0][lo:hi])
+
+
+def test_attention_length_errors_between_prompts():
+    """Sequences whose lengths do not fit, between prompts of many row blocks."""
+    torch = _torch()
+    import precision_gemm_amd as P
+    print("[case] lengths that do not fit between prompts", flush=True)
+    b = Batch(15, [150, 200, 90], [150, 333, 90], 8, 2, 64, 16, False)
+    for wrong in (10, 0, -7):
+        was, b.kvs = b.kvs, [150, wrong, 90]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = b.run(status=status)
+        b.kvs = was
+        assert status.item() == P.LORA_ATTN_BAD_LENGTH
+        assert not out[150:350].any() and (lse[150:350] == float("-inf")).all()
+        for rows in (slice(0, 150), slice(350, 440)):
+            b.check(out, lse, rows)
 
 
 def test_attention_same_bits_whatever_the_workspace():
