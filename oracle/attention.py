@@ -77,7 +77,7 @@ def tree_attention(q, k_cache, v_cache, page_table, kv_len, q_indptr, masks, sca
     """(out [T, n_q, D], lse [T, n_q], weighted [T, n_q, D], spread [T, n_q]): the attention of
     each drafted token; ``masks`` per token a Python integer of the drafted tokens it sees, or
     None for causal order.  ``weighted`` is the softmax average of |V| and ``spread`` the largest
-    sum of |q||k| scale, the scales of the rounding errors that a checker allows for.  Keys that
+    sum of |q||k| scale, the scales of the rounding errors that a test allows for.  Keys that
     a token does not see do not enter, whatever they hold."""
     q = np.asarray(q, np.float64)
     T, n_q, D = q.shape
