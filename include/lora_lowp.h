@@ -492,7 +492,9 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
  * What the cache holds in keys that a token does not see, NaN included, does not reach it.
  * Keys in pages outside [0, n_pages) count as not seen; a sequence whose n_b is outside
  * [0, max_q] or reaches past T is left out; one whose kv_len is below n_b or past its pages is
- * taken as empty. */
+ * taken as empty.  Rows that no sequence has (a batch padded to T rows, or a sequence left out)
+ * get out 0, lse -inf and LORA_ATTN_BAD_LENGTH, as lora_tree_mask gives them masks of 0.  T, B or
+ * max_q of 0: nothing is done, rows included. */
 lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, const void* k_cache,
                                 const void* v_cache, const float* k_scale, const float* v_scale, int32_t n_pages,
                                 int32_t page_size, const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,

@@ -122,9 +122,9 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``q`` bf16 [T, n_q, D]; ``page_table`` int32 [B, max pages], ``kv_len`` int32 [B] (the drafted
     tokens included), ``q_indptr`` int32 [B + 1], ``max_q`` at least every sequence's drafted tokens;
     ``tree_mask`` int64 or uint64 [T, words] (None: in order).  Returns ``(out, lse)``, bf16
-    [T, n_q, D] and float32 [T, n_q].  With ``workspace`` (uint8, any content, at least
-    :func:`tree_attention_workspace_bytes`; calls that overlap in time need their own), ``out`` and
-    ``lse`` passed in the call allocates nothing."""
+    [T, n_q, D] and float32 [T, n_q]; rows that no sequence has are 0 and -inf.  With ``workspace``
+    (uint8, any content, at least :func:`tree_attention_workspace_bytes`; calls that overlap in time
+    need their own), ``out`` and ``lse`` passed in the call allocates nothing."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _done("lora_tree_attention", _c().tree_attention(q, k_cache, v_cache, page_table, kv_len, q_indptr, max_q,

@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 #include <initializer_list>
+#include <limits>
 #include <stdexcept>
 #include <string>
 
@@ -312,6 +313,11 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         words, (float)number(a[8]), static_cast<uint16_t*>(po), static_cast<float*>(ps), status_word(a[14], dev), pw,
         (size_t)ws.numel(), stream(a[15]));
     if (s != LORA_OK) return status(s);
+    if (T > 0 && (B == 0 || max_q == 0)) {  // the library does nothing here; what it returns is defined all the same
+      out.zero_();
+      lse.fill_(-std::numeric_limits<double>::infinity());
+      if (const Tensor* word = opt(a[14], "status")) word->bitwise_or_(LORA_ATTN_BAD_LENGTH);
+    }
     return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
   });
 }

@@ -122,7 +122,8 @@ __device__ __forceinline__ int step_weight(int rows) { return !SHARED ? 1 : rows
 
 // One sequence: its queries and keys, its steps, row blocks (the last one's steps count `last`),
 // and what the steps of one kv head's units count together.
-struct Seq { int q0, n, kv, steps, blocks, last, head, bad; };
+struct Seq { int q0, n, kv, steps, blocks, last, head, bad; };  // bad: EMPTY, LEFT_OUT
+enum { EMPTY = 1, LEFT_OUT = 2 };
 // Steps of row block rb of 128 rows, and of the blocks before it.  In order, `group` blocks hold 128
 // tokens, so that every `group` blocks a block's last token sees a step more.
 __device__ __forceinline__ bool in_order(const TreeAttnParams& p, const Seq& s) { return p.counted && s.kv >= s.n; }
@@ -143,6 +144,11 @@ __device__ __forceinline__ int block_at(const TreeAttnParams& p, const Seq& s, i
   return m * p.group + (x - steps_before(p, s, m * p.group)) / steps_of(p, s, m * p.group);
 }
 
+// Whether a sequence's rows [q0, q1) lie in the call's and are not more than it allows for.
+__device__ __forceinline__ bool tokens_fit(int q0, int q1, int T, int max_q) {
+  return q0 >= 0 && q1 >= q0 && q1 <= T && q1 - q0 <= max_q;
+}
+
 template <bool SHARED>
 __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1, int kv, int block_rows) {
   Seq s;
@@ -150,8 +156,8 @@ __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1,
   s.kv = kv;
   s.bad = 0;
   s.n = q1 - q0;
-  if (q0 < 0 || q1 > p.T || s.n < 0 || s.n > p.max_q) { s.n = 0; s.bad = 1; }
-  if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad = 1; }
+  if (!tokens_fit(q0, q1, p.T, p.max_q)) { s.n = 0; s.bad = LEFT_OUT; }
+  if (kv < s.n || (long)kv > ((long)p.max_pages << p.page_log2)) { s.kv = 0; s.bad |= EMPTY; }
   s.steps = max(1, (s.kv + ATTN_KEYS - 1) / ATTN_KEYS);
   s.blocks = (s.n * p.group + block_rows - 1) / block_rows;
   s.last = step_weight<SHARED>(s.n * p.group - (s.blocks - 1) * block_rows);
@@ -165,30 +171,38 @@ __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1,
 // A workgroup's stretch [cur, end) of the line of all units' steps, `per` of it a workgroup, and
 // the sequence it begins in, from a prefix sum over the sequences' work that leaves cum[b], what
 // lies before sequence b, in LDS.  (Cutting every unit evenly instead, so that nobody begins a
-// second one, took a search that cost what it saved.)
-struct Stretch { int cur, end, per, b; Seq first; };
+// second one, took a search that cost what it saved.)  `loose`: rows that no sequence has (LOOSE),
+// some of them perhaps between sequences (LEFT_OUT).
+struct Stretch { int cur, end, per, b, loose; Seq first; };
+enum { LOOSE = 1 };
 template <int THREADS, bool SHARED>
-__device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int* wave_sum,
+__device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int2* wave_sum,
                                                 Stretch* found) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, each = (p.B + THREADS - 1) / THREADS;
-  int mine = 0;
+  int mine = 0, loose = 0;
   Seq s{};
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
     if (b < p.B) {
       s = make_seq<SHARED>(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
       if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
+      loose |= s.bad & LEFT_OUT;
       mine += p.n_kv * s.head;
       cum[b + 1] = mine;
     }
   }
+  if (tid == 0 && (p.q_indptr[0] != 0 || p.q_indptr[p.B] != p.T)) {
+    loose |= LOOSE;
+    if (blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
+  }
+  loose = (__any(loose & LOOSE) ? LOOSE : 0) | (__any(loose & LEFT_OUT) ? LEFT_OUT : 0);
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int u = __shfl_up(incl, d);
     if (lane >= d) incl += u;
   }
-  if (lane == 63) wave_sum[wave] = incl;
+  if (lane == 63) wave_sum[wave] = make_int2(incl, loose);
   if (tid == 0) {
     cum[0] = 0;
     found->cur = found->end = 0;  // for a workgroup past the end
@@ -197,9 +211,10 @@ __device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg,
   int before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) {
-    const int u = wave_sum[w];
-    before += w < wave ? u : 0;
-    total += u;
+    const int2 u = wave_sum[w];
+    before += w < wave ? u.x : 0;
+    total += u.x;
+    loose |= u.y;
   }
   // a step at least: a shorter stretch inside a unit may hold the beginning of none
   const int per = max((total + p.n_wg - 1) / p.n_wg, step_weight<SHARED>(min(p.max_q * p.group, block_rows)));
@@ -211,7 +226,7 @@ __device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg,
       const int next = before + cum[b + 1];
       if (from <= cur && cur < next) {
         if (each > 1) s = make_seq<SHARED>(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
-        *found = Stretch{cur, end, per, b, s};
+        *found = Stretch{cur, end, per, b, 0, s};
       }
       cum[b + 1] = next;
       from = next;
@@ -219,9 +234,32 @@ __device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg,
   }
   __syncthreads();
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  return Stretch{uniform(found->cur), uniform(found->end), uniform(found->per), uniform(found->b),
+  return Stretch{uniform(found->cur), uniform(found->end), uniform(found->per), uniform(found->b), uniform(loose),
                  Seq{uniform(found->first.q0), uniform(found->first.n), uniform(found->first.kv), uniform(found->first.steps),
                      uniform(found->first.blocks), uniform(found->first.last), uniform(found->first.head), 0}};
+}
+
+// Rows that no sequence has: out 0, lse -inf.  Each workgroup takes its share of all rows.  Unless a
+// sequence was left out they lie before the first one's and behind the last one's.
+template <int D, int THREADS>
+__device__ __forceinline__ void clear_loose(const TreeAttnParams& p, int wg, int loose) {
+  const int lo = p.q_indptr[0], hi = p.q_indptr[p.B];
+  for (int t = wg; t < p.T; t += p.n_wg) {
+    bool none = t < lo || t >= hi;
+    if (loose & LEFT_OUT) {
+      int taken = 0;
+      for (int b = threadIdx.x; b < p.B; b += THREADS) {
+        const int q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
+        taken |= tokens_fit(q0, q1, p.T, p.max_q) && q0 <= t && t < q1;
+      }
+      none = !__syncthreads_or(taken);
+    }
+    if (!none) continue;
+    uint4* row = reinterpret_cast<uint4*>(p.out + (long)t * p.n_q * D);
+    for (int c = threadIdx.x; c < p.n_q * (D / 8); c += THREADS) row[c] = zero4();
+    if (p.lse)
+      for (int h = threadIdx.x; h < p.n_q; h += THREADS) p.lse[(long)t * p.n_q + h] = NEG_INF;
+  }
 }
 
 // The scores of 32 keys of COUNT row tiles (S^T: lane (g, i) has keys 8 g .. 8 g + 7 of row i)
@@ -426,7 +464,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
   constexpr int OS = D + 4;        // row stride of the joining buffer (floats)
   __shared__ __attribute__((aligned(16))) float so[4 * 16 * OS];
   __shared__ float sml[4][RT * 16][2];
-  __shared__ int wave_sum[4];
+  __shared__ int2 wave_sum[4];
   __shared__ Stretch found;
   __shared__ uint64_t smask[64];  // the sequence's masks, where they are of one word
   // heads of 256: the queries are kept in LDS as operands, their registers hold keys and values
@@ -443,6 +481,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
 
   const Stretch mine = find_stretch<256, false>(p, wg, RT * 16, cum, wave_sum, &found);
   if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
+  if (mine.loose) clear_loose<D, 256>(p, wg, mine.loose);
   int cur = mine.cur, b = mine.b;
   Seq sq = mine.first;
   const int end = mine.end;
@@ -791,7 +830,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
   auto sv = [&](int gr, int tile) -> uint4& { return ops[GR * 2 * G::KS * 64 + (gr * NT + tile) * 64 + (threadIdx.x & 63)]; };
   __shared__ uint32_t s_odd[GR][PARTS / 2], s_bad[GR];
   __shared__ float2 sml[ROW_WAVES][16];
-  __shared__ int wave_sum[ROW_WAVES];
+  __shared__ int2 wave_sum[ROW_WAVES];
   __shared__ Stretch found;
   __shared__ uint64_t smask[64];  // the sequence's masks, where they are of one word
   extern __shared__ int cum[];
@@ -805,6 +844,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES, 2 * WGS) void k_tree_attention_rows
 
   const Stretch mine = find_stretch<64 * ROW_WAVES, true>(p, wg, BLOCK, cum, wave_sum, &found);
   if (tid == 0) p.desc[ATTN_DESC * wg] = 0;
+  if (mine.loose) clear_loose<D, 64 * ROW_WAVES>(p, wg, mine.loose);
   int cur = mine.cur, b = mine.b;
   int q0 = mine.first.q0, q1 = q0 + mine.first.n, kv_len = mine.first.kv;
   const int end = mine.end;
