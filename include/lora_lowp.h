@@ -484,6 +484,9 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
  *    (n_q % n_kv == 0);
  *  - page_table int32 [B][max_pages] (max_pages * page_size <= 2^30), kv_len int32 [B],
  *    q_indptr int32 [B + 1] (ascending, from 0 to T), max_q at least every n_b; B <= 4096;
+ *  - the call's size: with R = max_q n_q / n_kv rows of a sequence in blocks of 128 (R <= 32: 16), at
+ *    most N = min(B ceil(R / block), T n_q / (n_kv block) + min(B, T)) blocks, n_kv N
+ *    (max_pages page_size / 128 + 1) <= 5 * 10^8 (else LORA_ERR_UNSUPPORTED);
  *  - tree_mask uint64 [T][mask_words], max_q <= 64 mask_words, mask_words <= 16;
  *  - out bf16 [T][n_q D]; lse float [T][n_q] or NULL: the natural logarithm of the sum of
  *    exponentials.  A row that sees nothing (or only scores of -inf) gets out 0, lse -inf;
@@ -494,7 +497,9 @@ lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int3
  * [0, max_q] or reaches past T is left out; one whose kv_len is below n_b or past its pages is
  * taken as empty.  Rows that no sequence has (a batch padded to T rows, or a sequence left out)
  * get out 0, lse -inf and LORA_ATTN_BAD_LENGTH, as lora_tree_mask gives them masks of 0.  T, B or
- * max_q of 0: nothing is done, rows included. */
+ * max_q of 0: nothing is done, rows included.  Offsets that descend may give a row to several
+ * sequences: it gets the result of one of them; if the sequences have more than T rows in all,
+ * every one is left out. */
 lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, const void* k_cache,
                                 const void* v_cache, const float* k_scale, const float* v_scale, int32_t n_pages,
                                 int32_t page_size, const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,

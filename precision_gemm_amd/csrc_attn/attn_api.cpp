@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn_kernels.hpp"
 
 using namespace lora;
@@ -196,9 +198,11 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
   const int64_t rows = (int64_t)max_q * (n_q / n_kv);
   if (rows > INT32_MAX / 2) return LORA_ERR_UNSUPPORTED;
   const TreeAttnPlan pl = tree_attn_plan(D, max_q, n_q / n_kv, fp8, tree_mask != nullptr, (long)B * n_kv);
-  // all steps of a call, which count 3 at most, are numbered in 32 bits
-  const double steps = (double)B * n_kv * (double)((rows + pl.block_rows - 1) / pl.block_rows) *
-                       ((double)max_pages * page_size / ATTN_KEYS + 1.0);
+  // All steps of a call, which count 3 at most, are numbered in 32 bits.  Its row blocks are every
+  // sequence's at max_q rows, or what all T rows fill and a part one for each sequence that has any.
+  const double blocks = std::min((double)B * (double)((rows + pl.block_rows - 1) / pl.block_rows),
+                                 (double)T * (n_q / n_kv) / pl.block_rows + std::min(B, T));
+  const double steps = blocks * n_kv * ((double)max_pages * page_size / ATTN_KEYS + 1.0);
   if (steps > 5.0e8) return LORA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_tree_attention_workspace_bytes(n_q, n_kv, D, max_q))
     return LORA_ERR_WORKSPACE;

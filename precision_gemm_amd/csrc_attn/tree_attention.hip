@@ -172,50 +172,71 @@ __device__ __forceinline__ Seq make_seq(const TreeAttnParams& p, int q0, int q1,
 // the sequence it begins in, from a prefix sum over the sequences' work that leaves cum[b], what
 // lies before sequence b, in LDS.  (Cutting every unit evenly instead, so that nobody begins a
 // second one, took a search that cost what it saved.)  `loose`: rows that no sequence has (LOOSE),
-// some of them perhaps between sequences (LEFT_OUT).
+// some of them perhaps between sequences (LEFT_OUT), or all (NO_ROWS).
 struct Stretch { int cur, end, per, b, loose; Seq first; };
-enum { LOOSE = 1 };
+enum { LOOSE = 1, NO_ROWS = 4 };
 template <int THREADS, bool SHARED>
 __device__ __forceinline__ Stretch find_stretch(const TreeAttnParams& p, int wg, int block_rows, int* cum, int2* wave_sum,
                                                 Stretch* found) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, each = (p.B + THREADS - 1) / THREADS;
-  int mine = 0, loose = 0;
+  uint32_t mine = 0;  // the line's length has 31 bits, unless offsets give rows to several sequences
+  int loose = 0;
   Seq s{};
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
     if (b < p.B) {
-      s = make_seq<SHARED>(p, p.q_indptr[b], p.q_indptr[b + 1], p.kv_len[b], block_rows);
-      if (s.bad && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
-      loose |= s.bad & LEFT_OUT;
-      mine += p.n_kv * s.head;
-      cum[b + 1] = mine;
+      const int q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
+      s = make_seq<SHARED>(p, q0, q1, p.kv_len[b], block_rows);
+      const bool ends = (b == 0 && q0 != 0) || (b == p.B - 1 && q1 != p.T);
+      if ((s.bad || ends) && blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
+      loose |= (s.bad & LEFT_OUT) | (ends ? LOOSE : 0);
+      mine += (uint32_t)(p.n_kv * s.head);
+      cum[b + 1] = (int)mine;
     }
   }
-  if (tid == 0 && (p.q_indptr[0] != 0 || p.q_indptr[p.B] != p.T)) {
-    loose |= LOOSE;
-    if (blockIdx.x == 0 && p.status) or_agent(p.status, ST_LENGTH);
-  }
   loose = (__any(loose & LOOSE) ? LOOSE : 0) | (__any(loose & LEFT_OUT) ? LEFT_OUT : 0);
-  int incl = mine;
+  uint32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(incl, d);
+    const uint32_t u = __shfl_up(incl, d);
     if (lane >= d) incl += u;
   }
-  if (lane == 63) wave_sum[wave] = make_int2(incl, loose);
+  if (lane == 63) wave_sum[wave] = make_int2((int)incl, loose);
   if (tid == 0) {
     cum[0] = 0;
     found->cur = found->end = 0;  // for a workgroup past the end
   }
   __syncthreads();
-  int before = incl - mine, total = 0;
+  uint32_t ahead = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) {
     const int2 u = wave_sum[w];
-    before += w < wave ? u.x : 0;
-    total += u.x;
+    ahead += w < wave ? (uint32_t)u.x : 0u;
+    all += (uint32_t)u.x;
     loose |= u.y;
   }
+  if (loose & LEFT_OUT) {
+    // Descending offsets can give rows to several sequences, and the line more steps than the host
+    // has allowed for T rows: with more rows than T in all, every sequence is left out.
+    int rows = 0;
+    for (int i = 0; i < each; ++i) {
+      const int b = tid * each + i;
+      if (b >= p.B) continue;
+      const int q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
+      rows += tokens_fit(q0, q1, p.T, p.max_q) ? q1 - q0 : 0;  // 4,096 times 65,536 at most
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) rows += __shfl_xor(rows, d);
+    __syncthreads();  // the sums are read
+    if (lane == 0) wave_sum[wave].x = rows;
+    __syncthreads();
+    rows = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) rows += wave_sum[w].x;
+    if (rows > p.T) return Stretch{0, 0, 1, 0, LEFT_OUT | NO_ROWS, Seq{}};
+  }
+  int before = (int)ahead;
+  const int total = (int)all;
   // a step at least: a shorter stretch inside a unit may hold the beginning of none
   const int per = max((total + p.n_wg - 1) / p.n_wg, step_weight<SHARED>(min(p.max_q * p.group, block_rows)));
   const int cur = min(total, wg * per), end = min(total, cur + per);
@@ -245,8 +266,8 @@ template <int D, int THREADS>
 __device__ __forceinline__ void clear_loose(const TreeAttnParams& p, int wg, int loose) {
   const int lo = p.q_indptr[0], hi = p.q_indptr[p.B];
   for (int t = wg; t < p.T; t += p.n_wg) {
-    bool none = t < lo || t >= hi;
-    if (loose & LEFT_OUT) {
+    bool none = t < lo || t >= hi || (loose & NO_ROWS);
+    if ((loose & LEFT_OUT) && !(loose & NO_ROWS)) {
       int taken = 0;
       for (int b = threadIdx.x; b < p.B; b += THREADS) {
         const int q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];

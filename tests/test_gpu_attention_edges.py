@@ -109,3 +109,41 @@ def test_no_sequences_and_no_tokens_allowed():
         got = P.tree_attention(b.q, b.k, b.v, _i32(table), _i32(kvs), _i32(indptr), max_q, out=out, lse=lse, status=status)
         assert got[0] is out and not out.any() and (lse == float("-inf")).all()
         assert status.item() == P.LORA_ATTN_BAD_LENGTH
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompt_chunk_beside_decoding_sequences(fp8):
+    """A chunk of a prompt among 255 decoding sequences, with page tables for 131,072 tokens and room
+    for chunks of 8,192."""
+    import torch
+    import precision_gemm_amd as P
+    print("[case] chunk beside decoding sequences", fp8, flush=True)
+    ns, kvs = [1] * 256, [1 + 13 * b % 300 for b in range(256)]
+    ns[100], kvs[100] = 300, 700
+    b = Batch(33, ns, kvs, 32, 8, 64, 16, fp8, "none")
+    table = np.zeros((256, 8192), np.int64)
+    table[:, :b.table.shape[1]] = b.table
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sc = [None if s is None else torch.from_numpy(s).cuda() for s in (b.sk, b.sv)]
+    out, lse = P.tree_attention(b.q, b.k, b.v, _i32(table), _i32(kvs), _i32(b.indptr), 8192, scale=b.scale, k_scale=sc[0],
+                                v_scale=sc[1], status=status)
+    assert status.item() == 0
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("n_q,D,mask", [(4, 64, "none"), (4, 256, "none"), (64, 128, "none"), (32, 64, "tree")])
+def test_offsets_that_overlap(n_q, D, mask):
+    """Offsets that give the call's rows to several sequences, more rows than it has in all: every
+    sequence is left out."""
+    import torch
+    import precision_gemm_amd as P
+    print("[case] offsets that overlap", n_q, D, mask, flush=True)
+    ns, kvs = [1] * 40, [30] * 40
+    b = Batch(34, ns, kvs, n_q, 2, D, 16, False)
+    tm = torch.ones((40, 1), dtype=torch.int64, device="cuda") if mask == "tree" else None
+    for indptr in ([0, 40] * 20 + [0], [0, 21, 0, 20] + [40] * 37):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = _marked(b)
+        P.tree_attention(b.q, b.k, b.v, _i32(b.table), _i32([100] * 40), _i32(indptr), 40, tree_mask=tm, out=out, lse=lse, status=status)
+        assert status.item() == P.LORA_ATTN_BAD_LENGTH
+        assert not out.any() and (lse == float("-inf")).all()
