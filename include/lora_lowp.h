@@ -469,7 +469,8 @@ lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* 
  * among its own sequence's drafted tokens, before its own; negative: the token follows the
  * cached prefix), q_indptr int32 [B + 1] as below -> mask uint64 [T][words], bit i % 64 of word
  * i / 64 set for the token itself and its ancestors.  max_q <= 64 words, words <= 16.  Rows of
- * no sequence, and of one whose tokens do not fit (LORA_ATTN_BAD_LENGTH), are 0. */
+ * no sequence, and of one whose tokens do not fit (LORA_ATTN_BAD_LENGTH), are 0; a sequence that
+ * fits keeps its rows where another's offsets run over them. */
 lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t B, int32_t T, int32_t max_q,
                            int32_t words, uint64_t* mask, int32_t* status, void* stream);
 

@@ -1188,8 +1188,18 @@ __global__ __launch_bounds__(256) void k_tree_mask(const int* parents, const int
   __shared__ uint64_t bits[2][MASK_MOST];
   __shared__ short up[2][MASK_MOST];
   const int b = blockIdx.x, w = blockIdx.y, q0 = q_indptr[b], q1 = q_indptr[b + 1];
-  auto clear = [&](int from, int to) {  // rows that no sequence has
-    for (int t = max(from, 0) + (int)threadIdx.x; t < min(to, T); t += 256) mask[(long)t * words + w] = 0;
+  auto clear = [&](int from, int to) {  // rows that no sequence has: of these, where offsets descend,
+    int back = 0;                       // those that no other sequence has
+    for (int o = threadIdx.x; o < B; o += 256) back |= q_indptr[o + 1] < q_indptr[o];
+    back = __syncthreads_or(back);
+    for (int t = max(from, 0) + (int)threadIdx.x; t < min(to, T); t += 256) {
+      bool taken = false;
+      for (int o = 0; back && o < B && !taken; ++o) {
+        const int o0 = q_indptr[o], o1 = q_indptr[o + 1];
+        taken = tokens_fit(o0, o1, T, max_q) && o0 <= t && t < o1;
+      }
+      if (!taken) mask[(long)t * words + w] = 0;
+    }
     if (threadIdx.x == 0 && status) or_agent(status, ST_LENGTH);
   };
   if (b == 0 && q0 > 0) clear(0, q0);

@@ -147,3 +147,28 @@ def test_offsets_that_overlap(n_q, D, mask):
         P.tree_attention(b.q, b.k, b.v, _i32(b.table), _i32([100] * 40), _i32(indptr), 40, tree_mask=tm, out=out, lse=lse, status=status)
         assert status.item() == P.LORA_ATTN_BAD_LENGTH
         assert not out.any() and (lse == float("-inf")).all()
+
+
+@pytest.mark.parametrize("indptr", [[4, 2, 6], [0, 6, 3], [0, 3, 0, 6], [5, 5, 2, 4, 1], [-3, 2, -1, 4], [600, 300, 900, 100]])
+def test_masks_of_offsets_that_descend(indptr):
+    """Rows of a sequence that fits keep their masks when another's offsets run over them; rows that
+    no sequence has are 0."""
+    import torch
+    import precision_gemm_amd as P
+    from oracle import attention as A
+    print("[case] masks, offsets that descend", indptr, flush=True)
+    T = 1000 if max(indptr) > 6 else 6
+    max_q = 4 if T == 6 else 600
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want, several = [0] * T, [0] * T
+    for lo, hi in zip(indptr[:-1], indptr[1:]):
+        if 0 <= lo <= hi <= T and hi - lo <= max_q:
+            want[lo:hi] = A.tree_mask(list(range(-1, hi - lo - 1)), [0, hi - lo])
+            for t in range(lo, hi):
+                several[t] += 1
+    assert max(several) <= 1
+    # every token the child of the one before in its own sequence (of the ones that fit)
+    parents = [max(0, w.bit_length() - 1) - 1 for w in want]
+    m = P.tree_mask(_i32(parents), _i32(indptr), max_q, status=status).cpu().numpy().view(np.uint64)
+    assert status.item() == P.LORA_ATTN_BAD_LENGTH
+    assert [sum(int(w) << 64 * i for i, w in enumerate(row)) for row in m] == want
