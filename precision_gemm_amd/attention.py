@@ -3,7 +3,7 @@ the append to a paged cache, and attention for drafted trees.
 
 The arguments are checked and marshalled by a compiled binding (csrc_attn/binding.cpp), built
 with the library by ``precision_gemm_amd.build``.  Every call enqueues on the current stream of
-its tensors' device and synchronises nothing.
+its tensors' device, whichever device is current, and synchronises nothing.
 """
 
 from __future__ import annotations
@@ -26,6 +26,7 @@ LORA_ATTN_BAD_PARENT = 16
 
 _binding = None
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() wraps it in an object: 2 us a call
+_current_device = torch._C._cuda_getDevice
 
 
 def _c():
@@ -38,16 +39,22 @@ def _c():
     return _binding
 
 
-def _stream(t) -> int:
-    """The current stream of a tensor's device (0 for what is no device tensor: the binding refuses it)."""
-    index = t.device.index if isinstance(t, torch.Tensor) else None
-    return 0 if index is None else _raw_stream(index)
-
-
-def _done(name: str, result):
-    """A call's outputs; the binding returns the library's status where it is an error."""
+def _call(name: str, on, *args):
+    """The binding's call ``name`` on the current stream of the device of tensor ``on``, with that
+    device current: the handle of a default stream is 0 on every device.  (What is no device tensor
+    the binding refuses.)  Returns the outputs; the binding returns the library's status where it is
+    an error."""
+    f = getattr(_c(), name)
+    index = on.device.index if isinstance(on, torch.Tensor) else None
+    if index is None:
+        result = f(*args, 0)
+    elif index == _current_device():
+        result = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            result = f(*args, _raw_stream(index))
     if type(result) is int:
-        check(name, result)
+        check("lora_" + name, result)
     return result
 
 
@@ -67,8 +74,8 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, n_q: int, n_
     rotation), ``q_weight`` and ``k_weight`` float32 [head_dim] (None: no norm).  Returns ``(q, k)``,
     bf16 [T, n_q, head_dim] and [T, n_kv, head_dim], in ``q_out`` and ``k_out`` if given (which may
     be the heads' own places in ``qkv``)."""
-    return _done("lora_qk_norm_rope", _c().qk_norm_rope(qkv, positions, n_q, n_kv, head_dim, cos_sin, q_weight, k_weight,
-                                                        eps, interleaved, q_out, k_out, status, _stream(qkv)))
+    return _call("qk_norm_rope", qkv, qkv, positions, n_q, n_kv, head_dim, cos_sin, q_weight, k_weight, eps, interleaved,
+                 q_out, k_out, status)
 
 
 def qk_norm_rope_backward_workspace_bytes(T: int, head_dim: int) -> int:
@@ -85,9 +92,8 @@ def qk_norm_rope_backward(qkv: torch.Tensor | None, positions: torch.Tensor | No
     :func:`lora_backward`, and float32 [D] (None without weights).  ``dv`` is copied to its place;
     with ``dv=None`` those columns of ``dqkv`` are left as they are (so ``dqkv`` has to be given).
     Output buffers and the workspace may be passed in; then the call allocates nothing."""
-    return _done("lora_qk_norm_rope_backward", _c().qk_norm_rope_backward(
-        qkv, positions, dq, dk, dv, cos_sin, q_weight, k_weight, eps, interleaved, dqkv, dq_weight, dk_weight, workspace,
-        status, _stream(dq)))
+    return _call("qk_norm_rope_backward", dq, qkv, positions, dq, dk, dv, cos_sin, q_weight, k_weight, eps, interleaved, dqkv,
+                 dq_weight, dk_weight, workspace, status)
 
 
 def rope_append_kv(qkv: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -98,15 +104,14 @@ def rope_append_kv(qkv: torch.Tensor, positions: torch.Tensor | None, slots: tor
     and ``v_cache`` [pages, kv heads, page size, D], bfloat16 or float8_e4m3fn (then ``k_scale`` and
     ``v_scale`` float32 [kv heads]); ``slots`` int32 [T], page * page size + offset (negative: not
     stored)."""
-    return _done("lora_rope_append_kv", _c().rope_append_kv(qkv, positions, slots, k_cache, v_cache, n_q, cos_sin, q_weight,
-                                                            k_weight, eps, interleaved, k_scale, v_scale, q_out, status,
-                                                            _stream(qkv)))
+    return _call("rope_append_kv", qkv, qkv, positions, slots, k_cache, v_cache, n_q, cos_sin, q_weight, k_weight, eps,
+                 interleaved, k_scale, v_scale, q_out, status)
 
 
 def tree_mask(parents: torch.Tensor, q_indptr: torch.Tensor, max_q: int, *, status=None) -> torch.Tensor:
     """Masks of drafted trees from their parents (lora_tree_mask): ``parents`` int32 [T] (index
     among the sequence's own drafted tokens, -1: none) -> int64 [T, ceil(max_q / 64)]."""
-    return _done("lora_tree_mask", _c().tree_mask(parents, q_indptr, max_q, status, _stream(parents)))
+    return _call("tree_mask", parents, parents, q_indptr, max_q, status)
 
 
 def tree_attention_workspace_bytes(n_q: int, n_kv: int, head_dim: int, max_q: int) -> int:
@@ -127,6 +132,5 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     need their own), ``out`` and ``lse`` passed in the call allocates nothing."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    return _done("lora_tree_attention", _c().tree_attention(q, k_cache, v_cache, page_table, kv_len, q_indptr, max_q,
-                                                            tree_mask, scale, k_scale, v_scale, out, lse, workspace, status,
-                                                            _stream(q)))
+    return _call("tree_attention", q, q, k_cache, v_cache, page_table, kv_len, q_indptr, max_q, tree_mask, scale, k_scale,
+                 v_scale, out, lse, workspace, status)

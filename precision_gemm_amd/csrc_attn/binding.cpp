@@ -3,8 +3,9 @@
 // on the GPU; the same binding through ctypes took 14 to 15 us of host time a call, four
 // times the work it launches, this one 6 to 7.
 //
-// Arguments come by position from precision_gemm_amd/attention.py, which documents them.  A
-// call returns its outputs, or the library's status as an int where that is not LORA_OK.
+// Arguments come by position from precision_gemm_amd/attention.py, which documents them and makes
+// the tensors' device current.  A call returns its outputs, or the library's status as an int
+// where that is not LORA_OK.
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
