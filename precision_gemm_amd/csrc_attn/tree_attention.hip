@@ -283,6 +283,22 @@ __device__ __forceinline__ void clear_loose(const TreeAttnParams& p, int wg, int
   }
 }
 
+// Waits until products that may still be writing these accumulators have written them.  The compiler
+// keeps that distance for instructions that it knows, not for ones in assembly: 24 wait states are
+// more than any product here takes.  Tied to the accumulators, so that their products come before.
+template <int NT>
+__device__ __forceinline__ void settle(v4f (&o)[NT]) {
+  if constexpr (NT == 4) {
+    asm volatile("s_nop 15\n\ts_nop 7" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]));
+  } else {
+    static_assert(NT % 8 == 0, "tiles by the eight");
+#pragma unroll
+    for (int t = 0; t < NT; t += 8)
+      asm volatile("s_nop 15\n\ts_nop 7"
+                   : "+v"(o[t]), "+v"(o[t + 1]), "+v"(o[t + 2]), "+v"(o[t + 3]), "+v"(o[t + 4]), "+v"(o[t + 5]), "+v"(o[t + 6]), "+v"(o[t + 7]));
+  }
+}
+
 // The scores of 32 keys of COUNT row tiles (S^T: lane (g, i) has keys 8 g .. 8 g + 7 of row i)
 // into the running softmax; pb: the probabilities as the MFMA operand of O^T = V^T P^T.
 // m, l, o: the first of the tiles'.
@@ -310,8 +326,8 @@ __device__ __forceinline__ void softmax_step(const v4f (&s)[COUNT][2], float sc,
       l[c] *= f;
       // in place, by hand: the compiler multiplies into other registers, and then has the way
       // around this branch, every step's, copy all of o (32 sequences of 2,048 keys, 256 rows, 8-bit
-      // cache: 139 us against 130).  The products that last wrote o are complete: the scores'
-      // products came behind them and have been read.
+      // cache: 139 us against 130)
+      settle<NT>(o[c]);
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
