@@ -60,6 +60,12 @@ double number(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) { PyErr_Clear(); throw Refused(std::string(name) + " must be a truth value"); }
+  return v == 1;
+}
+
 std::string list(at::IntArrayRef s) {
   std::string r = "[";
   for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + std::to_string(s[i]);
@@ -125,7 +131,7 @@ Rope rope(PyObject* positions, PyObject* cos_sin, PyObject* q_weight, PyObject* 
   r.qw = static_cast<float*>(need_or_null(qw, "q_weight", at::kFloat, {D}, dev));
   r.kw = static_cast<float*>(need_or_null(kw, "k_weight", at::kFloat, {D}, dev));
   r.eps = (float)number(eps);
-  r.interleaved = PyObject_IsTrue(interleaved) == 1;
+  r.interleaved = truth(interleaved, "interleaved");
   return r;
 }
 
