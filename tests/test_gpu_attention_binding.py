@@ -31,3 +31,21 @@ def test_interleaved_has_to_be_a_truth_value(value):
         P.rope_append_kv(qkv, pos, pos, cache, cache.clone(), n_q, cos_sin=cs, interleaved=what)
     q, _ = P.qk_norm_rope(qkv, pos, n_q, n_kv, D, cos_sin=cs, interleaved=np.bool_(True))
     assert q.shape == (3, n_q, D)
+
+
+def test_out_of_memory():
+    """Buffers that do not fit raise torch's own error, as every allocation of its does."""
+    import torch
+    import precision_gemm_amd as P
+    print("[case] out of memory", flush=True)
+    total = torch.cuda.mem_get_info()[1]
+    q = torch.zeros((16384, 8, 256), dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros((1, 1, 16, 256), dtype=torch.bfloat16, device="cuda")
+    one, two = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, 2))
+    torch.cuda.empty_cache()
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (8 << 20)) / total)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            P.tree_attention(q, cache, cache, one.view(1, 1), one, two, 1)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
