@@ -88,6 +88,16 @@ def test_many_sequences(B, most, n_q, n_kv, D, mask, fp8):
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("most,n_q,D", [(1, 2, 256), (3, 16, 256), (3, 16, 128)])
+def test_most_sequences_of_a_call(most, n_q, D, fp8):
+    """4,096 sequences, whose prefix sums are kept beside the largest buffers in LDS."""
+    print("[case] most sequences", most, n_q, D, fp8, flush=True)
+    ns = [1 + b % most for b in range(4096)]
+    b = Batch(43, ns, [n + b % 9 for b, n in enumerate(ns)], n_q, 1, D, 16, fp8, "none")
+    b.check(*b.run())
+
+
 SCALED = [  # ns, kvs, n_q, n_kv, D, mask: few rows a kv head, 17 to 32, more; one and two workgroups a CU
     ([1, 1, 1], [1, 300, 129], 8, 2, 128, "none"),
     ([4, 3], [4, 500], 8, 2, 64, "any"),
