@@ -3,7 +3,10 @@ the append to a paged cache, and attention for drafted trees.
 
 The arguments are checked and marshalled by a compiled binding (csrc_attn/binding.cpp), built
 with the library by ``precision_gemm_amd.build``.  Every call enqueues on the current stream of
-its tensors' device, whichever device is current, and synchronises nothing.
+its tensors' device, whichever device is current, and synchronises nothing.  They are no operations
+of autograd: outputs have no graph, whatever requires gradients among the inputs (the gradients of
+:func:`qk_norm_rope` are :func:`qk_norm_rope_backward`; the attention has none here), and buffers and
+caches are written without autograd's version counters.
 """
 
 from __future__ import annotations
@@ -73,7 +76,7 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, n_q: int, n_
     [T, (n_q + 2 n_kv) head_dim], rows of any stride; ``cos_sin`` from :func:`rope_table` (None: no
     rotation), ``q_weight`` and ``k_weight`` float32 [head_dim] (None: no norm).  Returns ``(q, k)``,
     bf16 [T, n_q, head_dim] and [T, n_kv, head_dim], in ``q_out`` and ``k_out`` if given (which may
-    be the heads' own places in ``qkv``)."""
+    be the heads' own places in ``qkv``); without a graph of autograd."""
     return _call("qk_norm_rope", qkv, qkv, positions, n_q, n_kv, head_dim, cos_sin, q_weight, k_weight, eps, interleaved,
                  q_out, k_out, status)
 
@@ -129,7 +132,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``tree_mask`` int64 or uint64 [T, words] (None: in order).  Returns ``(out, lse)``, bf16
     [T, n_q, D] and float32 [T, n_q]; rows that no sequence has are 0 and -inf.  With ``workspace``
     (uint8, any content, at least :func:`tree_attention_workspace_bytes`; calls that overlap in time
-    need their own), ``out`` and ``lse`` passed in the call allocates nothing."""
+    need their own), ``out`` and ``lse`` passed in the call allocates nothing.  The outputs have no graph of autograd."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _call("tree_attention", q, q, k_cache, v_cache, page_table, kv_len, q_indptr, max_q, tree_mask, scale, k_scale,

@@ -1,7 +1,7 @@
 // CPython binding of the attention block's calls on torch tensors: argument checks, output
-// allocation and marshalling, nothing else.  A decode step's append or head norm takes 3.5 us
+// allocation and marshalling, nothing else.  A decode step's append or head norm takes 3.2 us
 // on the GPU; the same binding through ctypes took 14 to 15 us of host time a call, four
-// times the work it launches, this one 6 to 7.
+// times the work it launches, this one 5.5 to 6.1.
 //
 // Arguments come by position from precision_gemm_amd/attention.py, which documents them and makes
 // the tensors' device current.  A call returns its outputs, or the library's status as an int

@@ -115,7 +115,11 @@ __device__ __forceinline__ uint32_t visible8(const TreeAttnParams& p, const uint
 
 // What a step of a unit counts on the line.  Where waves share the keys (SHARED, 128 rows a block)
 // a step of 64 rows or fewer takes them less time: 2.1 to 2.6 us against 3.5 (16 sequences with trees
-// of up to 64 tokens, 8-bit cache: 42.5 us with all steps alike, 36.5 so).
+// of up to 64 tokens over up to 2,048 keys, 8-bit cache: 42.5 us with all steps alike, 36.5 so).  How much
+// less depends on the cache and the heads; one weight for all is a compromise.  16 other sequences with
+// trees, calls in us, all alike and so: trees of up to 64, 8-bit cache, heads of 64 37.1 and 35.7, of
+// 128 56.4 and 58.1, of 256 97.2 and 94.4, 16-bit 41.7 and 43.3, 49.6 and 53.3, 95.5 and 100.6; trees of 16,
+// 16-bit, 21.8 and 21.7, 29.2 and 29.8, 61.4 and 55.8, 8-bit within 0.3.
 constexpr int FULL = 3, HALF_FULL = 2;
 template <bool SHARED>
 __device__ __forceinline__ int step_weight(int rows) { return !SHARED ? 1 : rows > 64 ? FULL : HALF_FULL; }
@@ -492,7 +496,7 @@ __device__ __forceinline__ void put_tile(const TreeAttnParams& p, int q0, int ro
 
 // Few rows: four waves split a step's 128 keys.  Bound by HBM: 64 sequences of up to 8,192 keys in
 // 16 bits, 4 rows a kv head (922 MB), 166 us, 5.5 TB/s; one of 131,072 in 8 bits 51 us, 5.3 TB/s.
-// Short work is bound by latencies: of the 16 us for 16 sequences of 1,024 keys (67 MB) the first
+// Short work is bound by latencies: of the 16.6 us for 16 sequences of 1,024 keys (67 MB) the first
 // 4 pass before keys are on their way (the launch, the prefix sum, the page table, the queries).
 template <int D, int RT, bool FP8, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attention(TreeAttnParams p) {
@@ -1314,7 +1318,12 @@ TreeAttnPlan tree_attn_plan(int D, int max_q, int group, bool fp8, bool mask, lo
     // prompts of 1,024 tokens, 4 of them, 147 and 120, of 4,096 465 and 304, of 700, 4, 96 and 75, of
     // 256, 32, 83 and 71; 800 more tokens of 8,000 178 and 170).  Not where all alike gives almost
     // every workgroup a unit of its own and cuts none (8 prompts of 256 30 and 43, 512 more tokens of
-    // 2,048, 4, 113 and 126), unless the prompts are long (2,048: 126 and 110).
+    // 2,048, 4, 113 and 126), unless the prompts are long (2,048: 126 and 110).  Units go by max_q, the
+    // one length that the host has.  In us, all alike and counted: 4 prompts of 256 19 and 30, on 2,000
+    // tokens each 67 and 81, two of 512 27 and 37, on 8,000 205 and 218; where the lengths are ragged the
+    // units are fewer and are cut all the same: 256, 100, 250 and 180 tokens 29 and 26, eight of 30 to
+    // 256 34 and 33, one of 256 beside three decoding sequences 39 and 38.  (Heads of 64 and 8-bit caches
+    // alike.)
     const bool own = units <= pl.n_wg && 8 * units > 7 * pl.n_wg && max_q < 1024;
     pl.counted = !mask && rows > pl.block_rows && !own;
   } else {
