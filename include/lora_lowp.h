@@ -512,6 +512,143 @@ lora_status lora_tree_attention(const uint16_t* q, int64_t ldq, int32_t kv_fmt, 
  * their lengths.  0 for heads it does not accept. */
 size_t lora_tree_attention_workspace_bytes(int32_t n_q, int32_t n_kv, int32_t D, int32_t max_q);
 
+/* ---- Rotation by positions of several axes ----
+ * The three calls above that rotate, for tokens with a position on each of n_axes axes (time,
+ * height and width of an image's patches; a text's tokens have them alike): pair i of a head turns
+ * by the angles of the position on axis pair_axes[i].
+ *  - positions int32 [n_axes][T], 1 <= n_axes <= 4;
+ *  - pair_axes [host] rot / 2 bytes, each below n_axes (read during the call).
+ * Everything else, the results of a token with a position outside the table included, is as for the
+ * calls with one position a token; the token counts as outside when any of its positions is. */
+lora_status lora_qk_norm_rope_axes(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                   const uint8_t* pair_axes, int32_t T, int32_t n_q, int32_t n_kv, int32_t D,
+                                   const float* cos_sin, int32_t max_pos, int32_t rot, int32_t interleaved,
+                                   const float* q_weight, const float* k_weight, float eps, uint16_t* q_out, int64_t ldq,
+                                   uint16_t* k_out, int64_t ldk, int32_t* status, void* stream);
+
+/* Its gradients; the workspace is that of lora_qk_norm_rope_backward. */
+lora_status lora_qk_norm_rope_axes_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                            const uint8_t* pair_axes, const uint16_t* dq, const uint16_t* dk,
+                                            const uint16_t* dv, int32_t T, int32_t n_q, int32_t n_kv, int32_t D,
+                                            const float* cos_sin, int32_t max_pos, int32_t rot, int32_t interleaved,
+                                            const float* q_weight, const float* k_weight, float eps, uint16_t* dqkv,
+                                            int64_t ldd, float* dq_weight, float* dk_weight, int32_t* status,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+lora_status lora_rope_axes_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                     const uint8_t* pair_axes, const int32_t* slots, int32_t T, int32_t n_q,
+                                     int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                                     int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                                     uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache, void* v_cache,
+                                     const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                                     int32_t* status, void* stream);
+
+/* ---- Norms of the hidden states in front of a projection ----
+ * For each of T rows of K values (rows of any stride, a multiple of 8 values; K % 8 == 0,
+ * K <= 16384; T == 0 is a no-op):
+ *     h = bf16(x + residual)  (x itself without a residual)
+ *     y = (h - mu) w / sqrt(mean((h - mu)^2) + eps) + b,  mu = mean(h), or 0 with rms = 1
+ *  - x, residual bf16 [T] rows of K (strides ldx, ldr); residual NULL: none;
+ *  - weight, bias float [K] or NULL (1 and 0);
+ *  - y bf16 [T] rows of K (ldy); sum: h, bf16 (lds), with a residual, else NULL.  y and sum may be
+ *    the rows of x or of the residual, each of them whole and in its own place; any other overlap is
+ *    not allowed.
+ * Statistics are those of the stored (rounded) h, in fp32, the squares summed about the mean; y is
+ * rounded once. */
+lora_status lora_layer_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, int32_t T, int32_t K,
+                            const float* weight, const float* bias, float eps, int32_t rms, uint16_t* y, int64_t ldy,
+                            uint16_t* sum, int64_t lds, void* stream);
+
+/* Gradients of lora_layer_norm.  With g = dy w, r = 1 / sqrt(mean((h - mu)^2) + eps), xh = (h - mu) r:
+ *     dx = r (g - mean(g) - xh mean(g xh)) + dsum   (without mean(g) for rms = 1)
+ *     dweight = sum over the rows of dy xh,  dbias = sum of dy
+ *  - dy bf16 [T] rows of K (lddy); h bf16 (ldh): the forward's sum, or its x without a residual;
+ *  - dsum bf16 (ldds) or NULL: the gradient that reaches h along the residual stream;
+ *  - dx bf16 (lddx): the gradient of x, and of the residual alike.  It may be dy's or dsum's rows in
+ *    their own places;
+ *  - dweight, dbias float [K], or NULL where not wanted (written, not accumulated into; zero for
+ *    T == 0), 16-byte aligned;
+ *  - workspace: lora_layer_norm_backward_workspace_bytes(T, K) bytes, in any state, when dweight or
+ *    dbias is wanted (partial sums, added in a fixed order: the result does not depend on timing). */
+lora_status lora_layer_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh,
+                                     const float* weight, const uint16_t* dsum, int64_t ldds, int32_t T, int32_t K,
+                                     float eps, int32_t rms, uint16_t* dx, int64_t lddx, float* dweight, float* dbias,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_layer_norm_backward; 0 for sizes it does not accept. */
+size_t lora_layer_norm_backward_workspace_bytes(int32_t T, int32_t K);
+
+/* ---- AdamW over many tensors at once: the step from lora_backward's gradients to the adapters ----
+ * A step takes any number of fp32 tensors, each of one of n_groups groups (a tenant: its adapters of
+ * all projections, and whatever else it trains), with per-group settings.  For a value p of gradient
+ * g, at step t of its group:
+ *     g' = g min(1, largest / (norm + 1e-6))                        (with norms)
+ *     m <- beta1 m + (1 - beta1) g',   v <- beta2 v + (1 - beta2) g'^2
+ *     p <- (1 - rate decay) p - rate (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * and writes p in bf16, as it is and in the forms that the layer and its backward read.  Arithmetic
+ * in fp32, every product and sum rounded on its own; the group's coefficients in fp64, rounded once. */
+enum {
+  LORA_ADAMW_PLAIN = 0, /* any tensor                                                              */
+  LORA_ADAMW_A = 1,     /* A [K][r]: pack = At of lora_pack_adapter, pack_bwd = Ar of lora_pack_adapter_bwd */
+  LORA_ADAMW_B = 2      /* B [r][N]: pack = Bt, pack_bwd = Bop                                      */
+};
+
+/* Bit of the step's status word. */
+enum { LORA_ADAMW_NOT_FINITE = 1 /* a group's gradient norm is not finite: the group is left as it was */ };
+
+/* One tensor of a step; addresses are device addresses, 16-byte aligned (scales: 4-byte). */
+typedef struct lora_adamw_tensor {
+  float* param;           /* [rows][cols], the master copy                                          */
+  const float* grad;      /* [rows][cols]                                                           */
+  void* m;                /* states: float [rows][cols] each; or, in 8 bits, e4m3fn codes: m = code */
+  void* v;                /*   * scale and sqrt(v) = code * scale, with one scale for each 64 values */
+  float* m_scale;         /* 8 bits: float [ceil(rows cols / 64)], of values in their order; else NULL */
+  float* v_scale;
+  uint16_t* copy;         /* bf16 [rows][cols], or NULL                                             */
+  uint16_t* pack;         /* the packed forms of A and B (see above), whole, padding ranks included, */
+  uint16_t* pack_bwd;     /*   or NULL                                                              */
+  int32_t rows, cols;     /* A: K, r; B: r, N.  K % 64 == 0, N % 64 == 0, 1 <= r <= 64; any sizes for */
+  int32_t group;          /*   a plain tensor; rows cols < 2^31                                     */
+  int32_t kind;
+} lora_adamw_tensor;
+
+typedef struct lora_adamw_tile { int32_t tensor, first; } lora_adamw_tile;
+
+/* Checks the tensors of a step and cuts them into tiles, once; a host function.  `tensors` [host] n
+ * of them (device addresses inside); *n_tiles [host] receives the number of tiles.  With tiles [host]
+ * not NULL (*n_tiles of them, from a call with NULL before) they are written, in the groups' order,
+ * and group_first [host] int32 [n_groups + 1], each group's first.  The caller puts the tensors, tiles
+ * and group_first into device memory for lora_adamw_step.  LORA_ERR_INVALID_ARG also where a buffer
+ * that a step writes overlaps another of its buffers (a tensor given twice).
+ * Limits: n <= 2^20, n_groups <= 8192, fewer than 2^31 tiles. */
+lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t n_groups, int32_t state_bits,
+                            int64_t* n_tiles, lora_adamw_tile* tiles, int32_t* group_first);
+
+/* One step.
+ *  - tensors, tiles, group_first: from lora_adamw_plan, in device memory; state_bits 32 or 8, as there;
+ *  - hyper double [n_groups][6]: rate, beta1, beta2, eps, weight decay, largest gradient norm (0 or
+ *    less: not clipped);
+ *  - active int32 [n_groups] or NULL: groups that are 0 here are left as they are (a tenant without
+ *    tokens in the batch);
+ *  - steps int32 [n_groups]: the steps that each group has made, counted on by the groups that step;
+ *  - grad_norm float [n_groups] or NULL.  With it, each active group's gradient norm (fp64 sums in a
+ *    fixed order) is written there (0 for the others), gradients are clipped by it, and a group whose
+ *    norm is not finite is left as it was, with LORA_ADAMW_NOT_FINITE in *status.  Without it there is
+ *    no clipping, and gradients that are not finite reach the states;
+ *  - status device int32 or NULL (OR-ed in);
+ *  - workspace: lora_adamw_workspace_bytes bytes, in any state.
+ * States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to
+ * nearest even, and the scale largest / 448; blocks whose largest magnitude is below 2^-100 as zero;
+ * a root of v that is not 0 keeps a code that is not (a code of 0 would let the next step grow to
+ * m / eps).  The step itself uses m and v before that rounding. */
+lora_status lora_adamw_step(const lora_adamw_tensor* tensors, const lora_adamw_tile* tiles, int64_t n_tiles,
+                            const int32_t* group_first, int32_t n_groups, int32_t state_bits, const double* hyper,
+                            const int32_t* active, int32_t* steps, float* grad_norm, int32_t* status, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_adamw_step; 0 for sizes it does not accept. */
+size_t lora_adamw_workspace_bytes(int64_t n_tiles, int32_t n_groups);
+
 /* Device-side status word of the layer calls on this workspace since it was last
  * initialised (bits accumulate): copies one int32 to *status_dev (device pointer) on
  * `stream`.  0 = fine; bit 0 = a bounded wait in the fused launch gave up (the output

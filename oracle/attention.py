@@ -3,7 +3,8 @@ rotation, their gradients, the append to a paged cache, drafted trees and attent
 cache.  Written from the definitions; shares no code with the HIP path.
 
 ``cos_sin`` is the rotation table [positions, rot] (rot / 2 cosines, then the sines).  Heads
-are [T, heads, D]; a paged cache is [pages, kv heads, page size, D].
+are [T, heads, D]; a paged cache is [pages, kv heads, page size, D].  ``positions`` are [T], or
+with ``axes`` (an axis for each pair) [axes, T].
 """
 
 from __future__ import annotations
@@ -18,7 +19,7 @@ def _pairs(rot: int, interleaved: bool):
     return (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
 
 
-def rotate(x, positions, cos_sin, interleaved=False, sign=1.0):
+def rotate(x, positions, cos_sin, interleaved=False, sign=1.0, axes=None):
     """Each head's pairs turned by sign times the position's angles."""
     y = np.array(x, np.float64)
     if cos_sin is None:
@@ -26,23 +27,28 @@ def rotate(x, positions, cos_sin, interleaved=False, sign=1.0):
     cos_sin = np.asarray(cos_sin, np.float64)
     rot = cos_sin.shape[1]
     a, b = _pairs(rot, interleaved)
-    c, s = cos_sin[positions, :rot // 2][:, None, :], sign * cos_sin[positions, rot // 2:][:, None, :]
+    if axes is None:
+        angles = cos_sin[positions]
+    else:  # pair i by its own axis
+        row, pair = np.asarray(positions)[list(axes)].T, np.arange(rot // 2)
+        angles = np.concatenate([cos_sin[row, pair], cos_sin[row, rot // 2 + pair]], 1)
+    c, s = angles[:, None, :rot // 2], sign * angles[:, None, rot // 2:]
     ya, yb = y[..., a].copy(), y[..., b].copy()
     y[..., a], y[..., b] = ya * c - yb * s, yb * c + ya * s
     return y
 
 
-def norm_rope(x, positions, cos_sin, weight, eps, interleaved=False):
+def norm_rope(x, positions, cos_sin, weight, eps, interleaved=False, axes=None):
     """Norm (weight not None) and rotation of heads [T, H, D]."""
     x = np.asarray(x, np.float64)
     if weight is not None:
         x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
-    return rotate(x, positions, cos_sin, interleaved)
+    return rotate(x, positions, cos_sin, interleaved, axes=axes)
 
 
-def norm_rope_backward(x, dy, positions, cos_sin, weight, eps, interleaved=False):
+def norm_rope_backward(x, dy, positions, cos_sin, weight, eps, interleaved=False, axes=None):
     """(dx, dweight) of :func:`norm_rope` (dweight None without a weight)."""
-    g = rotate(dy, positions, cos_sin, interleaved, sign=-1.0)
+    g = rotate(dy, positions, cos_sin, interleaved, sign=-1.0, axes=axes)
     if weight is None:
         return g, None
     x = np.asarray(x, np.float64)

@@ -13,5 +13,7 @@ from .ops import (  # noqa: F401
 from .attention import (  # noqa: F401
     LORA_ATTN_BAD_LENGTH, LORA_ATTN_BAD_PAGE, LORA_ATTN_BAD_PARENT, LORA_ATTN_BAD_POSITION, LORA_ATTN_BAD_SLOT,
     LORA_KV_BF16, LORA_KV_FP8_E4M3, qk_norm_rope, qk_norm_rope_backward, qk_norm_rope_backward_workspace_bytes,
-    rope_append_kv, rope_table, tree_attention, tree_attention_workspace_bytes, tree_mask,
+    rope_append_kv, rope_pair_axes, rope_table, tree_attention, tree_attention_workspace_bytes, tree_mask,
 )
+from .norm import layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes  # noqa: F401
+from .optimizer import LORA_ADAMW_NOT_FINITE, AdamW, AdamWTensor, adamw_adapters, adamw_step  # noqa: F401

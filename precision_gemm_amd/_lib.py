@@ -19,6 +19,12 @@ _lib = None
 c_i32, c_u32, c_size, c_vp = ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_void_p
 c_i64, c_f32 = ctypes.c_int64, ctypes.c_float
 
+class AdamWTensorStruct(ctypes.Structure):
+    """lora_adamw_tensor."""
+    _fields_ = [(n, c_vp) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy", "pack", "pack_bwd")] + [
+        (n, c_i32) for n in ("rows", "cols", "group", "kind")]
+
+
 _SIGNATURES = {
     "lora_status_string": (ctypes.c_char_p, [c_i32]),
     "lora_version": (ctypes.c_char_p, []),
@@ -60,6 +66,22 @@ _SIGNATURES = {
                                     c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_f32, c_vp, c_vp, c_vp,
                                     c_vp, c_size, c_vp]),
     "lora_tree_attention_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32]),
+    "lora_qk_norm_rope_axes": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32,
+                                       c_vp, c_vp, c_f32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "lora_qk_norm_rope_axes_backward": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32,
+                                                c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_f32, c_vp, c_i64, c_vp, c_vp, c_vp,
+                                                c_vp, c_size, c_vp]),
+    "lora_rope_axes_append_kv": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32,
+                                         c_i32, c_vp, c_vp, c_f32, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                         c_vp, c_vp]),
+    "lora_layer_norm": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_f32, c_i32, c_vp, c_i64, c_vp, c_i64,
+                                c_vp]),
+    "lora_layer_norm_backward": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_i32, c_i32, c_f32, c_i32, c_vp, c_i64,
+                                         c_vp, c_vp, c_vp, c_size, c_vp]),
+    "lora_layer_norm_backward_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "lora_adamw_plan": (c_i32, [c_vp, c_i32, c_i32, c_i32, ctypes.POINTER(c_i64), c_vp, c_vp]),
+    "lora_adamw_step": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "lora_adamw_workspace_bytes": (c_size, [c_i64, c_i32]),
     "lora_plan_info": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i32), c_i32]),
 }
 

@@ -69,16 +69,29 @@ def rope_table(max_pos: int, rot: int, theta: float = 10000.0, device="cuda") ->
     return torch.cat([a.cos(), a.sin()], 1).to(torch.float32).to(device)
 
 
+def rope_pair_axes(sections, interleaved: bool = False) -> bytes:
+    """``pair_axes`` of the calls below for positions of several axes: ``sections[a]`` of a head's
+    rotated pairs turn by axis a, one section after another, or (``interleaved``) the axes taken in
+    turn over the pairs until each has its number."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError("sections must be one to four numbers of pairs")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
 def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, n_q: int, n_kv: int, head_dim: int, *, cos_sin=None,
                  q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
-                 status=None):
+                 status=None, pair_axes=None):
     """Norms of the query and key heads and their rotation (lora_qk_norm_rope).  ``qkv`` bf16
     [T, (n_q + 2 n_kv) head_dim], rows of any stride; ``cos_sin`` from :func:`rope_table` (None: no
-    rotation), ``q_weight`` and ``k_weight`` float32 [head_dim] (None: no norm).  Returns ``(q, k)``,
+    rotation); with ``pair_axes`` (bytes, :func:`rope_pair_axes`) tokens have a position on each of up to
+    four axes, ``positions`` int32 [axes, T], and each pair turns by its axis's; ``q_weight`` and ``k_weight`` float32 [head_dim] (None: no norm).  Returns ``(q, k)``,
     bf16 [T, n_q, head_dim] and [T, n_kv, head_dim], in ``q_out`` and ``k_out`` if given (which may
     be the heads' own places in ``qkv``); without a graph of autograd."""
     return _call("qk_norm_rope", qkv, qkv, positions, n_q, n_kv, head_dim, cos_sin, q_weight, k_weight, eps, interleaved,
-                 q_out, k_out, status)
+                 q_out, k_out, status, pair_axes)
 
 
 def qk_norm_rope_backward_workspace_bytes(T: int, head_dim: int) -> int:
@@ -89,26 +102,27 @@ def qk_norm_rope_backward_workspace_bytes(T: int, head_dim: int) -> int:
 def qk_norm_rope_backward(qkv: torch.Tensor | None, positions: torch.Tensor | None, dq: torch.Tensor, dk: torch.Tensor,
                           dv: torch.Tensor | None, *, cos_sin=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                           interleaved: bool = False, dqkv=None, dq_weight=None, dk_weight=None, workspace=None,
-                          status=None):
+                          status=None, pair_axes=None):
     """Gradients of :func:`qk_norm_rope` (lora_qk_norm_rope_backward): ``dq`` bf16 [T, n_q, D] and
     ``dk`` [T, n_kv, D] -> ``(dqkv, dq_weight, dk_weight)``: bf16 [T, (n_q + 2 n_kv) D], the dY of
     :func:`lora_backward`, and float32 [D] (None without weights).  ``dv`` is copied to its place;
     with ``dv=None`` those columns of ``dqkv`` are left as they are (so ``dqkv`` has to be given).
     Output buffers and the workspace may be passed in; then the call allocates nothing."""
     return _call("qk_norm_rope_backward", dq, qkv, positions, dq, dk, dv, cos_sin, q_weight, k_weight, eps, interleaved, dqkv,
-                 dq_weight, dk_weight, workspace, status)
+                 dq_weight, dk_weight, workspace, status, pair_axes)
 
 
 def rope_append_kv(qkv: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor, k_cache: torch.Tensor,
                    v_cache: torch.Tensor, n_q: int, *, cos_sin=None, q_weight=None, k_weight=None, eps: float = 1e-6,
-                   interleaved: bool = False, k_scale=None, v_scale=None, q_out=None, status=None) -> torch.Tensor:
+                   interleaved: bool = False, k_scale=None, v_scale=None, q_out=None, status=None,
+                   pair_axes=None) -> torch.Tensor:
     """Keys and values of ``qkv`` into a paged cache (lora_rope_append_kv), the norm and rotation
     of :func:`qk_norm_rope` applied on the way; returns the queries, bf16 [T, n_q, D].  ``k_cache``
     and ``v_cache`` [pages, kv heads, page size, D], bfloat16 or float8_e4m3fn (then ``k_scale`` and
     ``v_scale`` float32 [kv heads]); ``slots`` int32 [T], page * page size + offset (negative: not
     stored)."""
     return _call("rope_append_kv", qkv, qkv, positions, slots, k_cache, v_cache, n_q, cos_sin, q_weight, k_weight, eps,
-                 interleaved, k_scale, v_scale, q_out, status)
+                 interleaved, k_scale, v_scale, q_out, status, pair_axes)
 
 
 def tree_mask(parents: torch.Tensor, q_indptr: torch.Tensor, max_q: int, *, status=None) -> torch.Tensor:

@@ -1,5 +1,5 @@
-"""Build the HIP library ``liblora_lowp.so`` in-tree for gfx950 with hipcc, and the attention
-block's Python binding ``_attn.so`` that links to it.
+"""Build the HIP library ``liblora_lowp.so`` in-tree for gfx950 with hipcc, and the Python bindings
+that link to it: ``_attn.so`` (the attention block) and ``_step.so`` (norms and the AdamW step).
 
 Run as ``python -m precision_gemm_amd.build``; ``__graft_entry__.build()`` calls
 :func:`build`.  Every call compiles (no up-to-date check), so a changed source is
@@ -21,6 +21,9 @@ SOURCES = ["lora_kernels.hip", "lora_gemm_pf.hip", "lora_backward.hip", "lora_ap
 # the attention block, apart from the layer's sources (whose hash names the layer's profiles)
 CSRC_ATTN = os.path.join(HERE, "csrc_attn")
 SOURCES_ATTN = ["rope_kernels.hip", "tree_attention.hip", "attn_api.cpp"]
+# norms and the optimizer's step
+CSRC_STEP = os.path.join(HERE, "csrc_step")
+SOURCES_STEP = ["norm_kernels.hip", "adamw_kernels.hip", "step_api.cpp"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops off: no v_pk_{add,mul,fma}_f32 in the device code.
@@ -35,7 +38,8 @@ FLAGS = [
     "-Rpass-analysis=kernel-resource-usage",
 ]
 RESOURCES = LIB + ".resources.json"
-BINDING = os.path.join(HERE, "_attn.so")
+BINDINGS = {os.path.join(HERE, "_attn.so"): os.path.join(CSRC_ATTN, "binding.cpp"),
+            os.path.join(HERE, "_step.so"): os.path.join(CSRC_STEP, "binding.cpp")}
 
 
 def parse_resources(stderr: str) -> dict:
@@ -64,7 +68,7 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     cmd = [hipcc(), *FLAGS, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES],
-           *[os.path.join(CSRC_ATTN, s) for s in SOURCES_ATTN]]
+           *[os.path.join(CSRC_ATTN, s) for s in SOURCES_ATTN], *[os.path.join(CSRC_STEP, s) for s in SOURCES_STEP]]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -78,30 +82,29 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     with open(RESOURCES, "w") as f:
         json.dump(parse_resources(res.stderr), f, indent=1, sort_keys=True)
-    build_binding(verbose)
+    for binding, source in BINDINGS.items():
+        build_binding(binding, source, verbose)
     return LIB
 
 
-def build_binding(verbose: bool = False) -> str:
-    """The attention block's binding (host code against the installed torch), beside the library
-    it calls."""
+def build_binding(binding: str, source: str, verbose: bool = False) -> None:
+    """A binding (host code against the installed torch), beside the library it calls."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
-    tmp = BINDING + ".tmp"
+    tmp = binding + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wno-attributes",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[f"-I{p}" for p in include_paths()], "-I" + sysconfig.get_paths()["include"],
-           os.path.join(CSRC_ATTN, "binding.cpp"), "-o", tmp, f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           source, "-o", tmp, f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
            *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"the binding's compilation failed ({res.returncode}):\n{res.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, binding)
 
 
 def resources() -> dict:

@@ -39,6 +39,29 @@ lora_status check_rope(const int32_t* positions, const float* cos_sin, int32_t m
   return LORA_OK;
 }
 
+// How a call gives its tokens' positions: one each (n 0), or on n axes, with an axis for each pair.
+struct Axes { int32_t n; const uint8_t* of_pair; };
+
+lora_status axis_map(const Axes& by, int32_t rot, AxisMap* m) {
+  m->n = by.n;
+  if (by.n == 0) return LORA_OK;
+  if (rot > 0 && !by.of_pair) return LORA_ERR_INVALID_ARG;
+  m->quads = 1;
+  for (int32_t i = 0; i < rot / 2; ++i) {
+    const uint64_t axis = by.of_pair[i];
+    if (axis >= (uint64_t)by.n) return LORA_ERR_INVALID_ARG;
+    m->pair[i / 32] |= axis << (2 * (i % 32));
+    if (i % 4 == 0) m->quad |= axis << (i / 2);
+    else if (axis != by.of_pair[i / 4 * 4]) m->quads = 0;
+  }
+  return LORA_OK;
+}
+
+// Calls that take axes take one at least, and four at most.
+inline lora_status check_axes(int32_t n) {
+  return n < 1 ? LORA_ERR_INVALID_ARG : n > 4 ? LORA_ERR_UNSUPPORTED : LORA_OK;
+}
+
 lora_status check_pages(int32_t n_pages, int32_t page_size, int32_t n_kv, int32_t* log2_out) {
   if (n_pages < 1 || page_size < 1) return LORA_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return LORA_ERR_UNSUPPORTED;
@@ -65,35 +88,32 @@ inline size_t plan_bytes(const TreeAttnPlan& pl) {
   return round256(pl.desc_bytes) + round256(pl.ml_bytes) + round256(pl.o_bytes);
 }
 
-}  // namespace
-
-extern "C" {
-
-lora_status lora_qk_norm_rope(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t T, int32_t n_q,
-                              int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
-                              int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
-                              uint16_t* q_out, int64_t ldq, uint16_t* k_out, int64_t ldk, int32_t* status,
-                              void* stream) {
+lora_status norm_rope(const uint16_t* qkv, int64_t ld, const int32_t* positions, const Axes& by, int32_t T,
+                      int32_t n_q, int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                      int32_t interleaved, const float* q_weight, const float* k_weight, float eps, uint16_t* q_out,
+                      int64_t ldq, uint16_t* k_out, int64_t ldk, int32_t* status, void* stream) {
+  AxisMap axes{};
   lora_status st = check_heads(T, n_q, n_kv, D);
   if (st != LORA_OK) return st;
   st = check_rope(positions, cos_sin, max_pos, rot, D, interleaved, q_weight, k_weight, eps);
   if (T == 0 && st != LORA_ERR_UNSUPPORTED) return LORA_OK;
-  if (st != LORA_OK) return st;
+  if (st != LORA_OK || (st = axis_map(by, rot, &axes)) != LORA_OK) return st;
   if (!rows_ok(qkv, ld, (int64_t)(n_q + 2 * n_kv) * D) || !rows_ok(q_out, ldq, (int64_t)n_q * D) ||
       !rows_ok(k_out, ldk, (int64_t)n_kv * D) || !aligned(status, 4))
     return LORA_ERR_INVALID_ARG;
   RopeParams p = rope_params(qkv, ld, positions, T, n_q, n_kv, cos_sin, max_pos, rot, interleaved, q_weight, k_weight,
                              eps, q_out, ldq, status);
-  p.k_out = k_out; p.ldk = ldk;
+  p.k_out = k_out; p.ldk = ldk; p.axes = axes;
   return launch_norm_rope(p, D, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
-lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* positions, const int32_t* slots,
-                                int32_t T, int32_t n_q, int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos,
-                                int32_t rot, int32_t interleaved, const float* q_weight, const float* k_weight,
-                                float eps, uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache, void* v_cache,
-                                const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
-                                int32_t* status, void* stream) {
+lora_status rope_append(const uint16_t* qkv, int64_t ld, const int32_t* positions, const Axes& by,
+                        const int32_t* slots, int32_t T, int32_t n_q, int32_t n_kv, int32_t D, const float* cos_sin,
+                        int32_t max_pos, int32_t rot, int32_t interleaved, const float* q_weight,
+                        const float* k_weight, float eps, uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache,
+                        void* v_cache, const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                        int32_t* status, void* stream) {
+  AxisMap axes{};
   lora_status st = check_heads(T, n_q, n_kv, D);
   if (st != LORA_OK) return st;
   int32_t lg = 0;
@@ -101,7 +121,7 @@ lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* 
   if ((st = check_pages(n_pages, page_size, n_kv, &lg)) != LORA_OK) return st;
   st = check_rope(positions, cos_sin, max_pos, rot, D, interleaved, q_weight, k_weight, eps);
   if (T == 0 && st != LORA_ERR_UNSUPPORTED) return LORA_OK;
-  if (st != LORA_OK) return st;
+  if (st != LORA_OK || (st = axis_map(by, rot, &axes)) != LORA_OK) return st;
   if (!rows_ok(qkv, ld, (int64_t)(n_q + 2 * n_kv) * D) || !rows_ok(q_out, ldq, (int64_t)n_q * D) || !slots ||
       !aligned(slots, 4) || !k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(status, 4))
     return LORA_ERR_INVALID_ARG;
@@ -111,24 +131,27 @@ lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* 
                              eps, q_out, ldq, status);
   p.slots = slots; p.k_cache = k_cache; p.v_cache = v_cache; p.k_scale = k_scale; p.v_scale = v_scale;
   p.page_log2 = lg; p.n_slots = (long)n_pages * page_size;
+  p.axes = axes;
   return launch_rope_append(p, D, fp8, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
-size_t lora_qk_norm_rope_backward_workspace_bytes(int32_t T, int32_t D) {
+size_t rope_backward_workspace(int32_t T, int32_t D) {
   if (T < 1 || T > MAX_TOKENS || (D != 64 && D != 128 && D != 256)) return 0;
   return (size_t)ROPE_BWD_WGS * D * sizeof(float);
 }
 
-lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, const uint16_t* dq,
-                                       const uint16_t* dk, const uint16_t* dv, int32_t T, int32_t n_q, int32_t n_kv,
-                                       int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
-                                       int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
-                                       uint16_t* dqkv, int64_t ldd, float* dq_weight, float* dk_weight,
-                                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+lora_status norm_rope_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, const Axes& by,
+                               const uint16_t* dq, const uint16_t* dk, const uint16_t* dv, int32_t T, int32_t n_q,
+                               int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                               int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                               uint16_t* dqkv, int64_t ldd, float* dq_weight, float* dk_weight, int32_t* status,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  AxisMap axes{};
   lora_status st = check_heads(T, n_q, n_kv, D);
   if (st != LORA_OK) return st;
   st = check_rope(positions, cos_sin, max_pos, rot, D, interleaved, q_weight, k_weight, eps);
   if (st == LORA_ERR_UNSUPPORTED || (st != LORA_OK && T > 0)) return st;
+  if (T > 0 && (st = axis_map(by, rot, &axes)) != LORA_OK) return st;
   const bool norm = q_weight != nullptr;
   if (norm && (!dq_weight || !dk_weight || !aligned(dq_weight, 16) || !aligned(dk_weight, 16))) return LORA_ERR_INVALID_ARG;
   RopeBwdParams p{};
@@ -138,14 +161,91 @@ lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const in
     if (!rows_ok(dqkv, ldd, width) || !dq || !dk || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
         !aligned(status, 4) || (norm && !rows_ok(qkv, ld, width)))
       return LORA_ERR_INVALID_ARG;
-    const size_t need = norm ? lora_qk_norm_rope_backward_workspace_bytes(T, D) : 0;
+    const size_t need = norm ? rope_backward_workspace(T, D) : 0;
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LORA_ERR_WORKSPACE;
   }
   p.qkv = qkv; p.ld = ld; p.positions = positions; p.n_q = n_q; p.n_kv = n_kv;
   p.cos_sin = cos_sin; p.max_pos = max_pos; p.rot = rot; p.interleaved = interleaved; p.eps = eps;
   p.dq = dq; p.dk = dk; p.dv = dv; p.dqkv = dqkv; p.ldd = ldd;
   p.part = reinterpret_cast<float*>(workspace); p.status = status;
+  p.axes = axes;
   return launch_norm_rope_bwd(p, D, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status lora_qk_norm_rope(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t T, int32_t n_q,
+                              int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                              int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                              uint16_t* q_out, int64_t ldq, uint16_t* k_out, int64_t ldk, int32_t* status,
+                              void* stream) {
+  return norm_rope(qkv, ld, positions, {0, nullptr}, T, n_q, n_kv, D, cos_sin, max_pos, rot, interleaved, q_weight,
+                   k_weight, eps, q_out, ldq, k_out, ldk, status, stream);
+}
+
+lora_status lora_qk_norm_rope_axes(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                   const uint8_t* pair_axes, int32_t T, int32_t n_q, int32_t n_kv, int32_t D,
+                                   const float* cos_sin, int32_t max_pos, int32_t rot, int32_t interleaved,
+                                   const float* q_weight, const float* k_weight, float eps, uint16_t* q_out, int64_t ldq,
+                                   uint16_t* k_out, int64_t ldk, int32_t* status, void* stream) {
+  const lora_status st = check_axes(n_axes);
+  if (st != LORA_OK) return st;
+  return norm_rope(qkv, ld, positions, {n_axes, pair_axes}, T, n_q, n_kv, D, cos_sin, max_pos, rot, interleaved,
+                   q_weight, k_weight, eps, q_out, ldq, k_out, ldk, status, stream);
+}
+
+lora_status lora_rope_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* positions, const int32_t* slots,
+                                int32_t T, int32_t n_q, int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos,
+                                int32_t rot, int32_t interleaved, const float* q_weight, const float* k_weight,
+                                float eps, uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache, void* v_cache,
+                                const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                                int32_t* status, void* stream) {
+  return rope_append(qkv, ld, positions, {0, nullptr}, slots, T, n_q, n_kv, D, cos_sin, max_pos, rot, interleaved,
+                     q_weight, k_weight, eps, q_out, ldq, kv_fmt, k_cache, v_cache, k_scale, v_scale, n_pages,
+                     page_size, status, stream);
+}
+
+lora_status lora_rope_axes_append_kv(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                     const uint8_t* pair_axes, const int32_t* slots, int32_t T, int32_t n_q,
+                                     int32_t n_kv, int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                                     int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                                     uint16_t* q_out, int64_t ldq, int32_t kv_fmt, void* k_cache, void* v_cache,
+                                     const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                                     int32_t* status, void* stream) {
+  const lora_status st = check_axes(n_axes);
+  if (st != LORA_OK) return st;
+  return rope_append(qkv, ld, positions, {n_axes, pair_axes}, slots, T, n_q, n_kv, D, cos_sin, max_pos, rot,
+                     interleaved, q_weight, k_weight, eps, q_out, ldq, kv_fmt, k_cache, v_cache, k_scale, v_scale,
+                     n_pages, page_size, status, stream);
+}
+
+size_t lora_qk_norm_rope_backward_workspace_bytes(int32_t T, int32_t D) { return rope_backward_workspace(T, D); }
+
+lora_status lora_qk_norm_rope_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, const uint16_t* dq,
+                                       const uint16_t* dk, const uint16_t* dv, int32_t T, int32_t n_q, int32_t n_kv,
+                                       int32_t D, const float* cos_sin, int32_t max_pos, int32_t rot,
+                                       int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+                                       uint16_t* dqkv, int64_t ldd, float* dq_weight, float* dk_weight,
+                                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  return norm_rope_backward(qkv, ld, positions, {0, nullptr}, dq, dk, dv, T, n_q, n_kv, D, cos_sin, max_pos, rot,
+                            interleaved, q_weight, k_weight, eps, dqkv, ldd, dq_weight, dk_weight, status, workspace,
+                            workspace_bytes, stream);
+}
+
+lora_status lora_qk_norm_rope_axes_backward(const uint16_t* qkv, int64_t ld, const int32_t* positions, int32_t n_axes,
+                                            const uint8_t* pair_axes, const uint16_t* dq, const uint16_t* dk,
+                                            const uint16_t* dv, int32_t T, int32_t n_q, int32_t n_kv, int32_t D,
+                                            const float* cos_sin, int32_t max_pos, int32_t rot, int32_t interleaved,
+                                            const float* q_weight, const float* k_weight, float eps, uint16_t* dqkv,
+                                            int64_t ldd, float* dq_weight, float* dk_weight, int32_t* status,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  const lora_status st = check_axes(n_axes);
+  if (st != LORA_OK) return st;
+  return norm_rope_backward(qkv, ld, positions, {n_axes, pair_axes}, dq, dk, dv, T, n_q, n_kv, D, cos_sin, max_pos,
+                            rot, interleaved, q_weight, k_weight, eps, dqkv, ldd, dq_weight, dk_weight, status,
+                            workspace, workspace_bytes, stream);
 }
 
 lora_status lora_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t B, int32_t T, int32_t max_q,

@@ -9,11 +9,19 @@
 
 namespace lora {
 
+// Positions of several axes: pair i of a head turns by the position on axis (pair[i / 32] >> 2 (i % 32)) & 3.
+struct AxisMap {
+  uint64_t pair[4];
+  uint64_t quad;           // the same for each four pairs, where all quads have one axis
+  int n;                   // axes; 0: one position a token
+  int quads;               // each quad of pairs has one axis
+};
+
 // Head norm and rotation, forward (k_out) and into the paged cache (k_cache).
 struct RopeParams {
   const uint16_t* qkv;     // bf16 [T][ld]: n_q, n_kv, n_kv heads of D
   long ld;
-  const int* positions;
+  const int* positions;    // [T], or [axes.n][T]
   int T, n_q, n_kv;
   const float* cos_sin;    // [max_pos][rot]: rot / 2 cosines, then the sines
   int max_pos, rot, interleaved;
@@ -30,6 +38,7 @@ struct RopeParams {
   long n_slots;
   int* status;
   int rounds_q, rounds_k;  // waves over a token's query heads, key (and value) heads
+  AxisMap axes;
 };
 
 struct RopeBwdParams {
@@ -49,6 +58,7 @@ struct RopeBwdParams {
   int* status;
   int rounds_q, rounds_k;            // rounds of a wave over a token's query heads, key heads
   int q_wg, n_wg;                    // workgroups of the query heads, of all
+  AxisMap axes;
 };
 
 constexpr int ROPE_BWD_WGS = 768;    // most workgroups of the backward (three a CU) and rows of its partial sums

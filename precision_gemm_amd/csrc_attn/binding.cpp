@@ -6,125 +6,42 @@
 // Arguments come by position from precision_gemm_amd/attention.py, which documents them and makes
 // the tensors' device current.  A call returns its outputs, or the library's status as an int
 // where that is not LORA_OK.
-#include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/pybind.h>
-
-#include <ATen/ATen.h>
-#include <initializer_list>
-#include <limits>
-#include <stdexcept>
-#include <string>
-
-#include "../../include/lora_lowp.h"
+#include "binding_util.hpp"
 
 namespace {
 
-using at::Tensor;
-
-struct Refused : std::runtime_error { using std::runtime_error::runtime_error; };
-
-const char* type_name(at::ScalarType t) {
-  switch (t) {
-    case at::kBFloat16: return "torch.bfloat16";
-    case at::kFloat: return "torch.float32";
-    case at::kInt: return "torch.int32";
-    case at::kByte: return "torch.uint8";
-    default: return c10::toString(t);
-  }
-}
-
-const Tensor* opt(PyObject* o, const char* name) {
-  if (o == Py_None) return nullptr;
-  if (!THPVariable_Check(o)) throw Refused(std::string(name) + " must be a tensor");
-  return &THPVariable_Unpack(o);
-}
-const Tensor& req(PyObject* o, const char* name) {
-  const Tensor* t = opt(o, name);
-  if (!t) throw Refused(std::string(name) + " must be a tensor");
-  return *t;
-}
-
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) { PyErr_Clear(); throw Refused("sizes must be integers"); }
-  return v;
-}
-int32_t int32(PyObject* o) {
-  const int64_t v = integer(o);
-  if (v < INT32_MIN || v > INT32_MAX) throw Refused("sizes must fit 32 bits");
-  return (int32_t)v;
-}
-double number(PyObject* o) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) { PyErr_Clear(); throw Refused("scale and eps must be numbers"); }
-  return v;
-}
-
-bool truth(PyObject* o, const char* name) {
-  const int v = PyObject_IsTrue(o);
-  if (v < 0) { PyErr_Clear(); throw Refused(std::string(name) + " must be a truth value"); }
-  return v == 1;
-}
-
-std::string list(at::IntArrayRef s) {
-  std::string r = "[";
-  for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + std::to_string(s[i]);
-  return r + "]";
-}
-
-void on_device(const Tensor& t, const char* name, const at::Device& dev) {
-  if (dev.type() != at::kCUDA) throw Refused(std::string(name) + " must be a device tensor");
-  if (t.device() != dev) throw Refused(std::string(name) + " must be on " + dev.str() + ", got " + t.device().str());
-}
-
-// Address of a dense device tensor of this type and shape.
-void* need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, const at::Device& dev) {
-  if (t.scalar_type() != type)
-    throw Refused(std::string(name) + " must have dtype " + type_name(type) + ", got " + type_name(t.scalar_type()));
-  if (t.sizes() != shape) throw Refused(std::string(name) + " must have shape " + list(shape) + ", got " + list(t.sizes()));
-  on_device(t, name, dev);
-  if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
-  return t.data_ptr();
-}
-void* need_or_null(const Tensor* t, const char* name, at::ScalarType type, at::IntArrayRef shape, const at::Device& dev) {
-  return t ? need(*t, name, type, shape, dev) : nullptr;
-}
-
-struct Rows { uint16_t* p; int64_t ld; };
-// bf16 rows [T, width] (or [T, heads, D]) of any stride, their values dense within a row.
-Rows rows(const Tensor& t, const char* name, int64_t width, int64_t T, const at::Device& dev) {
-  if (t.scalar_type() != at::kBFloat16)
-    throw Refused(std::string(name) + " must have dtype torch.bfloat16, got " + type_name(t.scalar_type()));
-  on_device(t, name, dev);
-  const int64_t d = t.dim();
-  if ((d != 2 && d != 3) || t.size(0) != T || (d == 2 ? t.size(1) : t.size(1) * t.size(2)) != width)
-    throw Refused(std::string(name) + " must be " + std::to_string(T) + " rows of " + std::to_string(width) + " values, got " + list(t.sizes()));
-  if (T > 0 && ((t.size(d - 1) > 1 && t.stride(d - 1) != 1) || (d == 3 && t.size(1) > 1 && t.stride(1) != t.size(2))))
-    throw Refused(std::string(name) + " must be dense within each row");
-  return {static_cast<uint16_t*>(t.data_ptr()), T > 1 ? t.stride(0) : width};
-}
-
-Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-}
-
 // The rotation's arguments.
 struct Rope {
+  int32_t n_axes = 0;  // 0: one position a token
+  const uint8_t* pair_axes = nullptr;
   const int32_t* pos = nullptr;
   const float* table = nullptr;
   int32_t max_pos = 0, rot = 0, interleaved = 0;
   const float *qw = nullptr, *kw = nullptr;
   float eps = 0.f;
 };
-Rope rope(PyObject* positions, PyObject* cos_sin, PyObject* q_weight, PyObject* k_weight, PyObject* eps, PyObject* interleaved,
-          int64_t T, int64_t D, const at::Device& dev) {
+Rope rope(PyObject* positions, PyObject* pair_axes, PyObject* cos_sin, PyObject* q_weight, PyObject* k_weight, PyObject* eps,
+          PyObject* interleaved, int64_t T, int64_t D, const at::Device& dev) {
   Rope r;
+  if (pair_axes != Py_None && cos_sin == Py_None) throw Refused("pair_axes is for a rotation: it needs cos_sin");
   if (const Tensor* t = opt(cos_sin, "cos_sin")) {
     if (t->dim() != 2 || t->size(0) > INT32_MAX || t->size(1) > INT32_MAX) throw Refused("cos_sin must be [positions, rot]");
     r.max_pos = (int32_t)t->size(0);
     r.rot = (int32_t)t->size(1);
     r.table = static_cast<float*>(need(*t, "cos_sin", at::kFloat, {r.max_pos, r.rot}, dev));
-    r.pos = static_cast<int32_t*>(need(req(positions, "positions"), "positions", at::kInt, {T}, dev));
+    const Tensor& pos = req(positions, "positions");
+    if (pair_axes == Py_None) {
+      r.pos = static_cast<int32_t*>(need(pos, "positions", at::kInt, {T}, dev));
+    } else {
+      if (!PyBytes_Check(pair_axes) || PyBytes_GET_SIZE(pair_axes) != r.rot / 2)
+        throw Refused("pair_axes must be bytes, an axis for each of the " + std::to_string(r.rot / 2) + " pairs");
+      if (pos.dim() != 2 || pos.size(0) < 1 || pos.size(0) > 4) throw Refused("with pair_axes, positions must be [1 to 4 axes, tokens]");
+      r.n_axes = (int32_t)pos.size(0);
+      r.pair_axes = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(pair_axes));
+      for (int32_t i = 0; i < r.rot / 2; ++i)
+        if (r.pair_axes[i] >= r.n_axes) throw Refused("pair_axes names axis " + std::to_string(r.pair_axes[i]) + " of " + std::to_string(r.n_axes));
+      r.pos = static_cast<int32_t*>(need(pos, "positions", at::kInt, {r.n_axes, T}, dev));
+    }
   }
   const Tensor *qw = opt(q_weight, "q_weight"), *kw = opt(k_weight, "k_weight");
   if (!qw != !kw) throw Refused("q_weight and k_weight go together");
@@ -156,62 +73,34 @@ Cache cache(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, const at::
   return c;
 }
 
-int32_t tokens(const Tensor& t, const char* name) {
-  if (t.dim() < 1 || t.size(0) > INT32_MAX) throw Refused(std::string(name) + " has no tokens' dimension");
-  return (int32_t)t.size(0);
-}
-int32_t* status_word(PyObject* o, const at::Device& dev) {
-  return static_cast<int32_t*>(need_or_null(opt(o, "status"), "status", at::kInt, {1}, dev));
-}
-void* stream(PyObject* o) { return PyLong_AsVoidPtr(o); }
-
-PyObject* status(lora_status s) { return PyLong_FromLong(s); }
-
-template <typename F>
-PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
-  try {
-    if (got != want) throw std::runtime_error("wrong number of arguments");
-    return f();
-  } catch (const Refused& e) {
-    PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const c10::OutOfMemoryError& e) {
-    // torch's own type (a RuntimeError), which callers that free memory and try again catch
-    PyObject* torch = PyImport_ImportModule("torch");
-    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
-    if (type) PyErr_SetString(type, e.what_without_backtrace());
-    Py_XDECREF(type);
-    Py_XDECREF(torch);
-  } catch (const c10::Error& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  }
-  return nullptr;
-}
-
-// qkv, positions, n_q, n_kv, D, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, status, stream -> (q, k)
+// qkv, positions, n_q, n_kv, D, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, status, pair_axes, stream
+// -> (q, k)
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 14, [&]() -> PyObject* {
+  return guarded(n, 15, [&]() -> PyObject* {
     const Tensor& qkv = req(a[0], "qkv");
     const int32_t T = tokens(qkv, "qkv"), n_q = int32(a[2]), n_kv = int32(a[3]), D = int32(a[4]);
     const at::Device dev = qkv.device();
     const Rows x = rows(qkv, "qkv", ((int64_t)n_q + 2ll * n_kv) * D, T, dev);
-    const Rope r = rope(a[1], a[5], a[6], a[7], a[8], a[9], T, D, dev);
+    const Rope r = rope(a[1], a[13], a[5], a[6], a[7], a[8], a[9], T, D, dev);
     const Tensor *qo = opt(a[10], "q_out"), *ko = opt(a[11], "k_out");
     if (n_q < 1 || n_kv < 1 || D < 1) return status(LORA_ERR_INVALID_ARG);
     const Tensor q = qo ? *qo : empty({T, n_q, D}, at::kBFloat16, dev), k = ko ? *ko : empty({T, n_kv, D}, at::kBFloat16, dev);
     const Rows ro = rows(q, "q_out", (int64_t)n_q * D, T, dev), rk = rows(k, "k_out", (int64_t)n_kv * D, T, dev);
-    const lora_status s = lora_qk_norm_rope(x.p, x.ld, r.pos, T, n_q, n_kv, D, r.table, r.max_pos, r.rot, r.interleaved, r.qw,
-                                            r.kw, r.eps, ro.p, ro.ld, rk.p, rk.ld, status_word(a[12], dev), stream(a[13]));
+    int32_t* word = status_word(a[12], dev);
+    const lora_status s =
+        r.n_axes ? lora_qk_norm_rope_axes(x.p, x.ld, r.pos, r.n_axes, r.pair_axes, T, n_q, n_kv, D, r.table, r.max_pos, r.rot,
+                                          r.interleaved, r.qw, r.kw, r.eps, ro.p, ro.ld, rk.p, rk.ld, word, stream(a[14]))
+                 : lora_qk_norm_rope(x.p, x.ld, r.pos, T, n_q, n_kv, D, r.table, r.max_pos, r.rot, r.interleaved, r.qw, r.kw,
+                                     r.eps, ro.p, ro.ld, rk.p, rk.ld, word, stream(a[14]));
     if (s != LORA_OK) return status(s);
     return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(k));
   });
 }
 
 // qkv, positions, dq, dk, dv, cos_sin, q_weight, k_weight, eps, interleaved, dqkv, dq_weight, dk_weight, workspace, status,
-// stream -> (dqkv, dq_weight, dk_weight)
+// pair_axes, stream -> (dqkv, dq_weight, dk_weight)
 PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 16, [&]() -> PyObject* {
+  return guarded(n, 17, [&]() -> PyObject* {
     const Tensor &dq = req(a[2], "dq"), &dk = req(a[3], "dk");
     if (dq.dim() != 3 || dk.dim() != 3) throw Refused("dq and dk must be [tokens, heads, head_dim]");
     const int32_t T = tokens(dq, "dq"), n_q = (int32_t)dq.size(1), n_kv = (int32_t)dk.size(1), D = (int32_t)dq.size(2);
@@ -221,7 +110,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pk = need(dk, "dk", at::kBFloat16, {T, n_kv, D}, dev);
     const Tensor* dv = opt(a[4], "dv");
     void* pv = need_or_null(dv, "dv", at::kBFloat16, {T, n_kv, D}, dev);
-    const Rope r = rope(a[1], a[5], a[6], a[7], a[8], a[9], T, D, dev);
+    const Rope r = rope(a[1], a[15], a[5], a[6], a[7], a[8], a[9], T, D, dev);
     const Rows x = r.qw ? rows(req(a[0], "qkv"), "qkv", width, T, dev) : Rows{nullptr, width};
     const Tensor* out = opt(a[10], "dqkv");
     if (!out && !dv) throw Refused("without dv, dqkv has to be given (its value columns are not written)");
@@ -234,12 +123,18 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dkw = kw ? *kw : empty({D}, at::kFloat, dev);
       ws = w ? *w : empty({std::max<int64_t>(16, (int64_t)lora_qk_norm_rope_backward_workspace_bytes(T, D))}, at::kByte, dev);
     }
-    const lora_status s = lora_qk_norm_rope_backward(
-        x.p, x.ld, r.pos, static_cast<uint16_t*>(pq), static_cast<uint16_t*>(pk), static_cast<uint16_t*>(pv), T, n_q, n_kv, D,
-        r.table, r.max_pos, r.rot, r.interleaved, r.qw, r.kw, r.eps, d.p, d.ld,
-        r.qw ? static_cast<float*>(need(dqw, "dq_weight", at::kFloat, {D}, dev)) : nullptr,
-        r.qw ? static_cast<float*>(need(dkw, "dk_weight", at::kFloat, {D}, dev)) : nullptr, status_word(a[14], dev),
-        r.qw ? need(ws, "workspace", at::kByte, {ws.numel()}, dev) : nullptr, r.qw ? (size_t)ws.numel() : 0, stream(a[15]));
+    float* gq = r.qw ? static_cast<float*>(need(dqw, "dq_weight", at::kFloat, {D}, dev)) : nullptr;
+    float* gk = r.qw ? static_cast<float*>(need(dkw, "dk_weight", at::kFloat, {D}, dev)) : nullptr;
+    int32_t* word = status_word(a[14], dev);
+    void* pw = r.qw ? need(ws, "workspace", at::kByte, {ws.numel()}, dev) : nullptr;
+    const size_t bytes = r.qw ? (size_t)ws.numel() : 0;
+    const uint16_t *g0 = static_cast<uint16_t*>(pq), *g1 = static_cast<uint16_t*>(pk), *g2 = static_cast<uint16_t*>(pv);
+    const lora_status s =
+        r.n_axes ? lora_qk_norm_rope_axes_backward(x.p, x.ld, r.pos, r.n_axes, r.pair_axes, g0, g1, g2, T, n_q, n_kv, D, r.table,
+                                                   r.max_pos, r.rot, r.interleaved, r.qw, r.kw, r.eps, d.p, d.ld, gq, gk, word,
+                                                   pw, bytes, stream(a[16]))
+                 : lora_qk_norm_rope_backward(x.p, x.ld, r.pos, g0, g1, g2, T, n_q, n_kv, D, r.table, r.max_pos, r.rot,
+                                              r.interleaved, r.qw, r.kw, r.eps, d.p, d.ld, gq, gk, word, pw, bytes, stream(a[16]));
     if (s != LORA_OK) return status(s);
     if (!r.qw) return Py_BuildValue("(NOO)", THPVariable_Wrap(dqkv), Py_None, Py_None);
     return Py_BuildValue("(NNN)", THPVariable_Wrap(dqkv), THPVariable_Wrap(dqw), THPVariable_Wrap(dkw));
@@ -247,23 +142,29 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // qkv, positions, slots, k_cache, v_cache, n_q, cos_sin, q_weight, k_weight, eps, interleaved, k_scale, v_scale, q_out, status,
-// stream -> q
+// pair_axes, stream -> q
 PyObject* rope_append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 16, [&]() -> PyObject* {
+  return guarded(n, 17, [&]() -> PyObject* {
     const Tensor& qkv = req(a[0], "qkv");
     const at::Device dev = qkv.device();
     const Cache c = cache(a[3], a[4], a[11], a[12], dev);
     const int32_t T = tokens(qkv, "qkv"), n_q = int32(a[5]);
     const Rows x = rows(qkv, "qkv", ((int64_t)n_q + 2ll * c.n_kv) * c.D, T, dev);
-    const Rope r = rope(a[1], a[6], a[7], a[8], a[9], a[10], T, c.D, dev);
+    const Rope r = rope(a[1], a[15], a[6], a[7], a[8], a[9], a[10], T, c.D, dev);
     const void* slots = need(req(a[2], "slots"), "slots", at::kInt, {T}, dev);
     if (n_q < 1 || c.n_kv < 1 || c.D < 1) return status(LORA_ERR_INVALID_ARG);
     const Tensor* qo = opt(a[13], "q_out");
     const Tensor q = qo ? *qo : empty({T, n_q, c.D}, at::kBFloat16, dev);
     const Rows ro = rows(q, "q_out", (int64_t)n_q * c.D, T, dev);
-    const lora_status s = lora_rope_append_kv(x.p, x.ld, r.pos, static_cast<const int32_t*>(slots), T, n_q, c.n_kv, c.D, r.table,
-                                              r.max_pos, r.rot, r.interleaved, r.qw, r.kw, r.eps, ro.p, ro.ld, c.fmt, c.k, c.v,
-                                              c.ks, c.vs, c.n_pages, c.page, status_word(a[14], dev), stream(a[15]));
+    const int32_t* at = static_cast<const int32_t*>(slots);
+    int32_t* word = status_word(a[14], dev);
+    const lora_status s =
+        r.n_axes ? lora_rope_axes_append_kv(x.p, x.ld, r.pos, r.n_axes, r.pair_axes, at, T, n_q, c.n_kv, c.D, r.table, r.max_pos,
+                                            r.rot, r.interleaved, r.qw, r.kw, r.eps, ro.p, ro.ld, c.fmt, c.k, c.v, c.ks, c.vs,
+                                            c.n_pages, c.page, word, stream(a[16]))
+                 : lora_rope_append_kv(x.p, x.ld, r.pos, at, T, n_q, c.n_kv, c.D, r.table, r.max_pos, r.rot, r.interleaved, r.qw,
+                                       r.kw, r.eps, ro.p, ro.ld, c.fmt, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, word,
+                                       stream(a[16]));
     if (s != LORA_OK) return status(s);
     return THPVariable_Wrap(q);
   });
@@ -336,7 +237,6 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-#define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(qk_norm_rope), ENTRY(qk_norm_rope_backward), ENTRY(rope_append_kv), ENTRY(tree_mask),
                          ENTRY(tree_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -63,6 +63,60 @@ __device__ __forceinline__ Turn load_turn(const float* cos_sin, int pos, int rot
   return t;
 }
 
+// How a token's positions are given: one; several, each quad of pairs on one axis; several, in any order.
+enum { ONE_AXIS = 0, AXIS_QUADS = 1, AXIS_PAIRS = 2 };
+
+// The positions of a token on each axis (0 where it is outside the table), and whether all are inside.
+template <int AXES>
+__device__ __forceinline__ bool load_positions(const int* positions, int T, int t, int max_pos, const AxisMap& axes,
+                                               int (&pos)[4]) {
+  bool placed = true;
+#pragma unroll
+  for (int a = 0; a < (AXES == ONE_AXIS ? 1 : 4); ++a) {
+    pos[a] = AXES == ONE_AXIS || a < axes.n ? positions[(long)a * T + t] : 0;
+    placed = placed && (unsigned)pos[a] < (unsigned)max_pos;
+  }
+  if (!placed) pos[0] = pos[1] = pos[2] = pos[3] = 0;
+  return placed;
+}
+
+// Rows of the table for this lane by its pairs' axes.  A quad of pairs on one axis is still one
+// 16-byte load of cosines and one of sines; otherwise every value is loaded by itself.
+template <int AXES>
+__device__ __forceinline__ Turn load_turn(const float* cos_sin, const int (&pos)[4], int rot, const LaneMap& m,
+                                          const AxisMap& axes) {
+  if (AXES == ONE_AXIS) return load_turn(cos_sin, pos[0], rot, m);
+  Turn t;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) { t.c[e] = 1.f; t.s[e] = 0.f; }
+  if (!m.turns) return t;
+  const int half = rot >> 1, p0 = pos[0], p1 = pos[1], p2 = pos[2], p3 = pos[3];
+  auto row = [=](int axis) {
+    const int lo = axis & 1 ? p1 : p0, hi = axis & 1 ? p3 : p2;
+    return cos_sin + (long)(axis & 2 ? hi : lo) * rot;
+  };
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int at = q ? m.t1 : m.t0;
+    if (AXES == AXIS_QUADS) {
+      const float* r = row((int)(axes.quad >> (at >> 1)) & 3) + at;
+      const float4 c = *reinterpret_cast<const float4*>(r), s = *reinterpret_cast<const float4*>(r + half);
+      t.c[4 * q] = c.x; t.c[4 * q + 1] = c.y; t.c[4 * q + 2] = c.z; t.c[4 * q + 3] = c.w;
+      t.s[4 * q] = s.x; t.s[4 * q + 1] = s.y; t.s[4 * q + 2] = s.z; t.s[4 * q + 3] = s.w;
+    } else {
+      const uint64_t w = at < 64 ? (at < 32 ? axes.pair[0] : axes.pair[1]) : (at < 96 ? axes.pair[2] : axes.pair[3]);
+      const int four = (int)(w >> (2 * (at & 31)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* r = row(four >> (2 * e)) + at + e;
+        t.c[4 * q + e] = r[0];
+        t.s[4 * q + e] = r[half];
+      }
+    }
+  }
+  return t;
+}
+
 // Turn the 16 values of a lane (chunk a in v[0..7], chunk b in v[8..15]); SIGN -1 turns back.
 template <int SIGN>
 __device__ __forceinline__ void turn(float (&v)[16], const Turn& t, int interleaved, bool turns) {
@@ -116,7 +170,7 @@ enum { FORWARD = 0, APPEND_BF16 = 1, APPEND_FP8 = 2 };
 // loads first, are slower up to 1,024 tokens (32 + 8 + 8 heads of 128, 16 tokens: 3.0 us, then 3.8,
 // 4.6 and 5.4) and no faster at 4,096 (21.7 us with inputs out of HBM, 4.0 TB/s; 22.6, 23.0, 23.9;
 // a copy of as many bytes 19.3).
-template <int D, int MODE>
+template <int D, int MODE, int AXES>
 __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH;
   const int lane = threadIdx.x & 63;
@@ -136,12 +190,9 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
     xa = ldg16(src + m.a);
     xb = ldg16(src + m.b);
   }
-  int pos = p.rot ? p.positions[t] : 0;
-  const bool placed = p.rot == 0 || (unsigned)pos < (unsigned)p.max_pos;
-  if (!placed) {
-    pos = 0;
-    if (p.status && lane == 0 && r == 0) or_agent(p.status, ST_POSITION);
-  }
+  int pos[4] = {0, 0, 0, 0};
+  const bool placed = p.rot == 0 || load_positions<AXES>(p.positions, p.T, t, p.max_pos, p.axes, pos);
+  if (!placed && p.status && lane == 0 && r == 0) or_agent(p.status, ST_POSITION);
   int slot = 0;
   if (MODE != FORWARD) {
     slot = p.slots[t];
@@ -151,7 +202,7 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
     }
     if (!placed) slot = -1;
   }
-  const Turn tn = load_turn(p.cos_sin, pos, p.rot, m);
+  const Turn tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes);
 
   float v[16];
   widen(xa, v);
@@ -202,7 +253,7 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
 // a workgroup, which k_weight_grad adds in order (no atomics: the result does not depend on
 // timing).  4,096 tokens of 32 + 8 + 8 heads of 128 (145 MB): 31.9 us, 4.5 TB/s; 512 workgroups
 // instead of 768 take 8 % longer, 256 55 %; two rounds in flight instead of one 3 %.
-template <int D>
+template <int D, int AXES>
 __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH, ROWS = 4 * SLOTS;
   __shared__ __attribute__((aligned(16))) float red[ROWS][D];
@@ -253,13 +304,10 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
     const Round now = next;
     const int t0 = t, r0 = r;
     if (fresh) {  // a token's first round here
-      int pos = p.rot ? p.positions[t0] : 0;
-      placed = p.rot == 0 || (unsigned)pos < (unsigned)p.max_pos;
-      if (!placed) {
-        pos = 0;
-        if (p.status && lane == 0) or_agent(p.status, ST_POSITION);
-      }
-      tn = load_turn(p.cos_sin, pos, p.rot, m);
+      int pos[4] = {0, 0, 0, 0};
+      placed = p.rot == 0 || load_positions<AXES>(p.positions, p.T, t0, p.max_pos, p.axes, pos);
+      if (!placed && p.status && lane == 0) or_agent(p.status, ST_POSITION);
+      tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes);
     }
     fresh = ++r == rounds;
     if (fresh) {
@@ -364,7 +412,10 @@ hipError_t launch_mode(RopeParams p, hipStream_t s) {
   p.rounds_q = (p.n_q + SLOTS - 1) / SLOTS;
   p.rounds_k = (p.n_kv + SLOTS - 1) / SLOTS;
   const int rounds = p.rounds_q + p.rounds_k + (MODE == FORWARD ? 0 : p.rounds_k);
-  hipLaunchKernelGGL((k_norm_rope<D, MODE>), dim3((unsigned)(((long)p.T * rounds + 3) / 4)), dim3(256), 0, s, p);
+  const dim3 grid((unsigned)(((long)p.T * rounds + 3) / 4));
+  if (p.axes.n == 0) hipLaunchKernelGGL((k_norm_rope<D, MODE, ONE_AXIS>), grid, dim3(256), 0, s, p);
+  else if (p.axes.quads) hipLaunchKernelGGL((k_norm_rope<D, MODE, AXIS_QUADS>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_norm_rope<D, MODE, AXIS_PAIRS>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -378,7 +429,11 @@ hipError_t launch_bwd(RopeBwdParams p, hipStream_t s) {
   const int rounds = p.rounds_q + 2 * p.rounds_k;
   p.q_wg = (int)std::min<long>(std::max(1, ROPE_BWD_WGS * p.rounds_q / rounds), ((long)p.T * p.rounds_q + 3) / 4);
   p.n_wg = p.q_wg + (int)std::min<long>(ROPE_BWD_WGS - ROPE_BWD_WGS * p.rounds_q / rounds, ((long)p.T * 2 * p.rounds_k + 3) / 4);
-  if (p.T > 0) hipLaunchKernelGGL(k_norm_rope_bwd<D>, dim3(p.n_wg), dim3(256), 0, s, p);
+  if (p.T > 0) {
+    if (p.axes.n == 0) hipLaunchKernelGGL((k_norm_rope_bwd<D, ONE_AXIS>), dim3(p.n_wg), dim3(256), 0, s, p);
+    else if (p.axes.quads) hipLaunchKernelGGL((k_norm_rope_bwd<D, AXIS_QUADS>), dim3(p.n_wg), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_norm_rope_bwd<D, AXIS_PAIRS>), dim3(p.n_wg), dim3(256), 0, s, p);
+  }
   if (p.q_weight)
     hipLaunchKernelGGL(k_weight_grad, dim3(2 * D / 16), dim3(1024), 0, s, p.part, p.q_wg, p.n_wg, D, p.dqw, p.dkw);
   return hipGetLastError();
