@@ -612,20 +612,24 @@ typedef struct lora_adamw_tensor {
   int32_t kind;
 } lora_adamw_tensor;
 
-typedef struct lora_adamw_tile { int32_t tensor, first; } lora_adamw_tile;
+/* A tile of a tensor: up to 4,096 of its values, from row (of A), column (of B) or value `first` on. */
+typedef struct lora_adamw_tile {
+  lora_adamw_tensor tensor;
+  int32_t first, reserved;
+} lora_adamw_tile;
 
 /* Checks the tensors of a step and cuts them into tiles, once; a host function.  `tensors` [host] n
  * of them (device addresses inside); *n_tiles [host] receives the number of tiles.  With tiles [host]
  * not NULL (*n_tiles of them, from a call with NULL before) they are written, in the groups' order,
- * and group_first [host] int32 [n_groups + 1], each group's first.  The caller puts the tensors, tiles
- * and group_first into device memory for lora_adamw_step.  LORA_ERR_INVALID_ARG also where a buffer
- * that a step writes overlaps another of its buffers (a tensor given twice).
+ * and group_first [host] int32 [n_groups + 1], each group's first.  The caller puts tiles and
+ * group_first into device memory for lora_adamw_step.  LORA_ERR_INVALID_ARG also where a buffer that a
+ * step writes overlaps another of its buffers (a tensor given twice).
  * Limits: n <= 2^20, n_groups <= 8192, fewer than 2^31 tiles. */
 lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t n_groups, int32_t state_bits,
                             int64_t* n_tiles, lora_adamw_tile* tiles, int32_t* group_first);
 
 /* One step.
- *  - tensors, tiles, group_first: from lora_adamw_plan, in device memory; state_bits 32 or 8, as there;
+ *  - tiles, group_first: from lora_adamw_plan, in device memory; state_bits 32 or 8, as there;
  *  - hyper double [n_groups][6]: rate, beta1, beta2, eps, weight decay, largest gradient norm (0 or
  *    less: not clipped);
  *  - active int32 [n_groups] or NULL: groups that are 0 here are left as they are (a tenant without
@@ -636,15 +640,15 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
  *    norm is not finite is left as it was, with LORA_ADAMW_NOT_FINITE in *status.  Without it there is
  *    no clipping, and gradients that are not finite reach the states;
  *  - status device int32 or NULL (OR-ed in);
- *  - workspace: lora_adamw_workspace_bytes bytes, in any state.
- * States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to
+ *  - workspace: lora_adamw_workspace_bytes bytes, zero-filled once before first use (every call leaves
+ *    its counters at zero again).
+ * A group without tensors makes no steps.  States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to
  * nearest even, and the scale largest / 448; blocks whose largest magnitude is below 2^-100 as zero;
  * a root of v that is not 0 keeps a code that is not (a code of 0 would let the next step grow to
  * m / eps).  The step itself uses m and v before that rounding. */
-lora_status lora_adamw_step(const lora_adamw_tensor* tensors, const lora_adamw_tile* tiles, int64_t n_tiles,
-                            const int32_t* group_first, int32_t n_groups, int32_t state_bits, const double* hyper,
-                            const int32_t* active, int32_t* steps, float* grad_norm, int32_t* status, void* workspace,
-                            size_t workspace_bytes, void* stream);
+lora_status lora_adamw_step(const lora_adamw_tile* tiles, int64_t n_tiles, const int32_t* group_first, int32_t n_groups,
+                            int32_t state_bits, const double* hyper, const int32_t* active, int32_t* steps,
+                            float* grad_norm, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of lora_adamw_step; 0 for sizes it does not accept. */
 size_t lora_adamw_workspace_bytes(int64_t n_tiles, int32_t n_groups);

@@ -80,7 +80,7 @@ _SIGNATURES = {
                                          c_vp, c_vp, c_vp, c_size, c_vp]),
     "lora_layer_norm_backward_workspace_bytes": (c_size, [c_i32, c_i32]),
     "lora_adamw_plan": (c_i32, [c_vp, c_i32, c_i32, c_i32, ctypes.POINTER(c_i64), c_vp, c_vp]),
-    "lora_adamw_step": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "lora_adamw_step": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
     "lora_adamw_workspace_bytes": (c_size, [c_i64, c_i32]),
     "lora_plan_info": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i32), c_i32]),
 }

@@ -22,116 +22,194 @@ namespace lora {
 namespace {
 
 enum { KIND_PLAIN = LORA_ADAMW_PLAIN, KIND_A = LORA_ADAMW_A, KIND_B = LORA_ADAMW_B };
-enum { C_B1, C_NB1, C_B2, C_NB2, C_EPS, C_ROOT, C_KEEP, C_RATE, C_CLIP, C_ON };
+// Values of a tile in LDS: of A, span rows of r + 4; of B, r rows of span + 8.
+constexpr int ADAMW_LDS = 5120;
 
 constexpr float E4M3_MAX = 448.f;
 constexpr float NO_SCALE = 0x1p-100f;  // blocks below it are held as zero: their scale's inverse would overflow
 
-// Values of a tile in LDS, its rows of an odd length: of A, span rows of r | 1, at most for r = 2
-// (2,048 rows of 3); of B, r rows of span + 1.
-constexpr int ADAMW_LDS = 6144;
-
-// A tile's place: `n4` quads of values, quad i at value `at(i)` of the tensor.
+// A tile's place: `n4` quads of values, quad i at value at(i) of the tensor.
 struct Place {
   long base;
-  int n4, len4;   // quads in all, and in a row of the tile
-  long ld;        // values from one row of the tile to the next
   int n;          // values in all (plain: the last quad may be part filled)
-  __device__ __forceinline__ long at(int i, int& row) const {
-    row = i / len4;
-    return base + row * ld + 4l * (i - row * len4);
+  int n4, len4;   // quads in all, and in a row of the tile
+  unsigned inv;   // 2^20 / len4, rounded up: i / len4 = i inv >> 20 for i < 1024
+  long ld;        // values from one row of the tile to the next
+  __device__ __forceinline__ int row(int i) const { return (int)((unsigned)i * inv >> 20); }
+  __device__ __forceinline__ long at(int i) const {
+    const int r = row(i);
+    return base + r * ld + 4 * (i - r * len4);
   }
 };
 
 __device__ __forceinline__ Place place(const lora_adamw_tensor& t, int first) {
   Place p;
-  if (t.kind == KIND_A) {          // rows first .. of [K][r], which lie together
-    const int rows = min(adamw_tile_span(t.cols), t.rows - first);
-    p.n = rows * t.cols;
-    p.base = (long)first * t.cols;
-    p.n4 = p.len4 = p.n / 4;
-    p.ld = 0;
-  } else if (t.kind == KIND_B) {   // columns first .. of [r][N]
+  if (t.kind == KIND_B) {   // columns first .. of [r][N]
     const int cols = min(adamw_tile_span(t.rows), t.cols - first);
     p.n = cols * t.rows;
     p.base = first;
-    p.n4 = p.n / 4;
     p.len4 = cols / 4;
+    p.inv = (1u << 20) / (unsigned)p.len4 + 1;
     p.ld = t.cols;
-  } else {
-    p.n = min((long)ADAMW_TILE, (long)t.rows * t.cols - first);
-    p.base = first;
-    p.n4 = p.len4 = (p.n + 3) / 4;
+  } else {                  // values that lie together: rows first .. of [K][r], or values of a vector
+    const bool a = t.kind == KIND_A;
+    p.n = a ? min(adamw_tile_span(t.cols), t.rows - first) * t.cols : (int)min((long)ADAMW_TILE, (long)t.rows * t.cols - first);
+    p.base = a ? (long)first * t.cols : first;
+    p.len4 = 0;
+    p.inv = 0;
     p.ld = 0;
   }
+  p.n4 = (p.n + 3) / 4;
   return p;
 }
 
-__device__ __forceinline__ float4 ld4(const float* p, int n) {  // the first n of 4 values
-  if (n >= 4) return *reinterpret_cast<const float4*>(p);
-  return make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, 0.f);
+// Addresses come out of memory: stated to be global ones, so that their loads and stores are (a flat
+// access also counts as one of LDS, whose waits would wait for it).
+// PAST: past the caches (see STREAM_TILES).
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+template <typename T, bool PAST = false>
+__device__ __forceinline__ T ldg(const void* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(1))) const T g_t;
+  g_t* at = (g_t*)(reinterpret_cast<uintptr_t>(p));
+  if constexpr (PAST) return __builtin_nontemporal_load(at);
+  else return *at;
+#else
+  return *reinterpret_cast<const T*>(p);  // host pass only; never executed
+#endif
 }
-__device__ __forceinline__ void st4(float* p, const float4& v, int n) {
-  if (n >= 4) {
-    *reinterpret_cast<float4*>(p) = v;
-  } else {
-    p[0] = v.x;
-    if (n > 1) p[1] = v.y;
-    if (n > 2) p[2] = v.z;
-  }
+template <bool PAST = false, typename T>
+__device__ __forceinline__ void stg(void* p, const T& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(1))) T g_t;
+  g_t* at = (g_t*)(reinterpret_cast<uintptr_t>(p));
+  if constexpr (PAST) __builtin_nontemporal_store(v, at);
+  else *at = v;
+#else
+  *reinterpret_cast<T*>(p) = v;
+#endif
 }
+
+__device__ __forceinline__ float4 as_float4(const f32x4& v) { return make_float4(v.x, v.y, v.z, v.w); }
+
+// Four values at p, or with PART the first n of them (a vector's last).
+template <bool PART, bool PAST>
+__device__ __forceinline__ float4 ld4(const float* p, int n) {
+  if (!PART || n >= 4) return as_float4(ldg<f32x4, PAST>(p));
+  return make_float4(n > 0 ? ldg<float>(p) : 0.f, n > 1 ? ldg<float>(p + 1) : 0.f, n > 2 ? ldg<float>(p + 2) : 0.f, 0.f);
+}
+template <bool PART, bool PAST>
 __device__ __forceinline__ uint32_t ld4(const uint8_t* p, int n) {
-  if (n >= 4) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t v = p[0];
-  if (n > 1) v |= (uint32_t)p[1] << 8;
-  if (n > 2) v |= (uint32_t)p[2] << 16;
+  if (!PART || n >= 4) return ldg<uint32_t, PAST>(p);
+  uint32_t v = 0;
+  for (int i = 0; i < n; ++i) v |= (uint32_t)ldg<uint8_t>(p + i) << (8 * i);
   return v;
 }
+template <bool PART, bool PAST>
+__device__ __forceinline__ void st4(float* p, const float (&v)[4], int n) {
+  if (!PART || n >= 4) return stg<PAST>(p, f32x4{v[0], v[1], v[2], v[3]});
+  if (n > 0) stg(p, v[0]);
+  if (n > 1) stg(p + 1, v[1]);
+  if (n > 2) stg(p + 2, v[2]);
+}
+template <bool PART, bool PAST>
 __device__ __forceinline__ void st4(uint8_t* p, uint32_t v, int n) {
-  if (n >= 4) {
-    *reinterpret_cast<uint32_t*>(p) = v;
-  } else {
-    for (int i = 0; i < n; ++i) p[i] = (uint8_t)(v >> (8 * i));
-  }
+  if (!PART || n >= 4) return stg<PAST>(p, v);
+  for (int i = 0; i < n; ++i) stg(p + i, (uint8_t)(v >> (8 * i)));
+}
+template <bool PART>
+__device__ __forceinline__ void st4(uint16_t* p, const uint2& v, int n) {
+  if (!PART || n >= 4) return stg(p, v);
+  if (n > 0) stg(p, (uint16_t)v.x);
+  if (n > 1) stg(p + 1, (uint16_t)(v.x >> 16));
+  if (n > 2) stg(p + 2, (uint16_t)v.y);
 }
 
-// Sums of the squares of a tile's gradients.
-__global__ __launch_bounds__(256) void k_adamw_norms(AdamWParams p) {
-  __shared__ double red[4];
-  const lora_adamw_tile tile = p.tiles[blockIdx.x];
-  const lora_adamw_tensor t = p.tensors[tile.tensor];
-  if (p.active && !p.active[t.group]) return;
-  const Place at = place(t, tile.first);
-  double s = 0.0;
-  for (int i = threadIdx.x; i < at.n4; i += 256) {
-    int row;
-    const float4 g = ld4(t.grad + at.at(i, row), at.n - 4 * i);
-    s += (double)g.x * g.x + (double)g.y * g.y + ((double)g.z * g.z + (double)g.w * g.w);
+// A group's coefficients at step t.
+struct Coef { float b1, nb1, b2, nb2, eps, root, keep, rate, clip; };
+
+__device__ __forceinline__ Coef coefficients(const double* h, int t, double clip) {
+  double p1 = 1.0, p2 = 1.0, q1 = h[1], q2 = h[2];  // beta1^t and beta2^t by squaring
+  for (int e = t; e > 0; e >>= 1) {
+    if (e & 1) { p1 *= q1; p2 *= q2; }
+    q1 *= q1;
+    q2 *= q2;
   }
+  Coef c;
+  c.b1 = (float)h[1];
+  c.nb1 = (float)(1.0 - h[1]);
+  c.b2 = (float)h[2];
+  c.nb2 = (float)(1.0 - h[2]);
+  c.eps = (float)h[3];
+  c.root = (float)(1.0 / sqrt(1.0 - p2));
+  c.keep = (float)(1.0 - h[0] * h[4]);
+  c.rate = (float)(h[0] / (1.0 - p1));
+  c.clip = (float)clip;
+  return c;
+}
+__device__ __forceinline__ void put(float* to, const Coef& c, bool on) {
+  to[0] = c.b1; to[1] = c.nb1; to[2] = c.b2; to[3] = c.nb2; to[4] = c.eps; to[5] = c.root; to[6] = c.keep; to[7] = c.rate;
+  to[8] = c.clip; to[9] = on ? 1.f : 0.f;
+}
+// The same through the scalar cache (an earlier launch wrote them).
+typedef __attribute__((address_space(4))) const float c_float;
+__device__ __forceinline__ Coef get(c_float* c) { return {c[0], c[1], c[2], c[3], c[4], c[5], c[6], c[7], c[8]}; }
+
+__device__ __forceinline__ double wave_sum(double s) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) p.part[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+  return s;
 }
 
-// A group's coefficients (and its norm, its tiles' sums joined in a fixed order); its step counts.
+// Sums of the squares of the tiles' gradients, a wave a tile, all its loads in flight at once.
+__global__ __launch_bounds__(256) void k_adamw_norms(AdamWParams p) {
+  const int lane = threadIdx.x & 63;
+  const long at = (long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (at >= p.n_tiles) return;
+  const lora_adamw_tile tile = p.tiles[at];
+  const lora_adamw_tensor& t = tile.tensor;
+  if (p.active && !p.active[t.group]) return;
+  const Place pl = place(t, tile.first);
+  const int full = pl.n >> 2;
+  f32x4 g[16];
+  // lanes without a quad read the tile's first: a load under a condition would wait for the one before
+  if (full) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int i = lane + 64 * k;
+      g[k] = ldg<f32x4>(t.grad + pl.at(i < full ? i : 0));
+    }
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const double q = ((double)g[k].x * g[k].x + (double)g[k].y * g[k].y) + ((double)g[k].z * g[k].z + (double)g[k].w * g[k].w);
+    s += lane + 64 * k < full ? q : 0.0;
+  }
+  if ((pl.n & 3) && lane == 0) {
+    const float4 e = ld4<true, false>(t.grad + pl.at(full), pl.n & 3);
+    s += (double)e.x * e.x + (double)e.y * e.y + (double)e.z * e.z;
+  }
+  s = wave_sum(s);
+  if (lane == 0) p.part[at] = s;
+}
+
+// A group's norm (its tiles' sums in a fixed order), step and coefficients.
 __global__ __launch_bounds__(256) void k_adamw_groups(AdamWParams p) {
   __shared__ double red[4];
-  const int g = blockIdx.x;
-  const bool active = !p.active || p.active[g];
-  double s = 0.0;
-  if (p.norm && active)
-    for (int i = p.group_first[g] + threadIdx.x; i < p.group_first[g + 1]; i += 256) s += p.part[i];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  const int g = blockIdx.x, first = p.group_first[g], last = p.group_first[g + 1];
+  bool on = (!p.active || p.active[g]) && first != last;
+  double clip = 1.0, s = 0.0;
+  const double* h = p.hyper + (long)g * ADAMW_HYPER;
+  const int step = p.steps[g] + 1;
+  if (p.norm && on) {
+#pragma unroll 8
+    for (int i = first + threadIdx.x; i < last; i += 256) s += p.part[i];
+  }
+  s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x) return;
-  const double* h = p.hyper + (long)g * ADAMW_HYPER;
-  float* c = p.coef + (long)g * ADAMW_COEF;
-  bool on = active;
-  double clip = 1.0;
   if (p.norm) {
     const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
     p.norm[g] = (float)norm;
@@ -141,33 +219,16 @@ __global__ __launch_bounds__(256) void k_adamw_groups(AdamWParams p) {
       if (p.status) or_agent(p.status, LORA_ADAMW_NOT_FINITE);
     }
   }
-  if (on) {
-    const int t = p.steps[g] + 1;
-    p.steps[g] = t;
-    double p1 = 1.0, p2 = 1.0, q1 = h[1], q2 = h[2];
-    for (int e = t; e > 0; e >>= 1) {
-      if (e & 1) { p1 *= q1; p2 *= q2; }
-      q1 *= q1;
-      q2 *= q2;
-    }
-    c[C_B1] = (float)h[1];
-    c[C_NB1] = (float)(1.0 - h[1]);
-    c[C_B2] = (float)h[2];
-    c[C_NB2] = (float)(1.0 - h[2]);
-    c[C_EPS] = (float)h[3];
-    c[C_ROOT] = (float)(1.0 / sqrt(1.0 - p2));
-    c[C_KEEP] = (float)(1.0 - h[0] * h[4]);
-    c[C_RATE] = (float)(h[0] / (1.0 - p1));
-    c[C_CLIP] = (float)clip;
-  }
-  c[C_ON] = on ? 1.f : 0.f;
+  if (on) p.steps[g] = step;
+  put(p.coef + (long)g * ADAMW_COEF, coefficients(h, step, clip), on);
 }
 
-__device__ __forceinline__ float sat448(float x) { return x != x ? x : fminf(fmaxf(x, -E4M3_MAX), E4M3_MAX); }
+// e4m3 codes, to nearest even.  No clamp: a value is at most its block's largest times 448 / largest, a
+// rounding or two above 448, which the conversion takes to 448 (what would round past it begins at 464).
 __device__ __forceinline__ uint32_t codes(const float (&v)[4]) {
   int r = 0;
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(sat448(v[0]), sat448(v[1]), r, false);
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(sat448(v[2]), sat448(v[3]), r, true);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], r, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
   return (uint32_t)r;
 }
 __device__ __forceinline__ void values(uint32_t c, float scale, float (&v)[4]) {
@@ -176,11 +237,17 @@ __device__ __forceinline__ void values(uint32_t c, float scale, float (&v)[4]) {
   v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c, 2) * scale;
   v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c, 3) * scale;
 }
-// Scale of a block from its 16 lanes' quads, and its inverse.
+// Scale of a block from its 16 lanes' quads (a row of lanes), and its inverse.
+template <int CTRL>
+__device__ __forceinline__ float row_max(float a) {
+  return fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, a), CTRL, 0xf, 0xf, true)));
+}
 __device__ __forceinline__ void block_scale(const float (&v)[4], float& scale, float& inv) {
   float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) a = fmaxf(a, __shfl_xor(a, d));
+  a = row_max<0xb1>(a);   // its neighbour
+  a = row_max<0x4e>(a);   // the other pair of four
+  a = row_max<0x141>(a);  // the other four of eight
+  a = row_max<0x140>(a);  // the other eight
   a = a >= NO_SCALE ? a : 0.f;
   scale = a * (1.f / E4M3_MAX);
   inv = a > 0.f ? 1.f / a * E4M3_MAX : 0.f;
@@ -202,147 +269,231 @@ __device__ __forceinline__ uint4 gather8(const uint16_t* s, int ld, int row, int
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A tile's values in the forms that the layer reads.  The tile in LDS has its ranks along the rows
-// (RANKS_ALONG: A, [k][j]) or along the columns (B, [j][n]); `first` is its place along the other
-// side, of `full` values, of which it has `span`.
-template <bool RANKS_ALONG>
-__device__ __forceinline__ void write_packs(const uint16_t* s, int ld, int r, int first, int span, int full, uint16_t* operand,
-                                            uint16_t* rows) {
-  if (operand) {  // MFMA operand order: rank tiles of 16, steps of 64 along the other side
-    const int steps = span / 64, chunks = (r + 15) / 16 * steps * 128;
-    for (int q = threadIdx.x; q < chunks; q += 256) {
-      const int l = q & 63, h = (q >> 6) & 1, st = (q >> 7) % steps, jt = (q >> 7) / steps;
-      const int j = 16 * jt + (l & 15), x = 64 * st + 16 * (l >> 4) + 8 * h;
-      const uint4 v = RANKS_ALONG ? gather8<false>(s, ld, x, j, j < r ? 8 : 0) : gather8<true>(s, ld, j, x, j < r ? 8 : 0);
-      *reinterpret_cast<uint4*>(operand + ((((long)jt * (full / 64) + first / 64 + st) * 2 + h) * 64 + l) * 8) = v;
+// The tile of A ([k][j], rows first .. of K) in At's order, from LDS; and in rows of ranks padded to a
+// multiple of 8, where those are not the tile as it is.
+template <int WG>
+__device__ __forceinline__ void write_packs_a(const uint16_t* s, int ld, int r, int first, int span, int K, uint16_t* operand,
+                                              uint16_t* rows) {
+  const int l = threadIdx.x & 63, h = (threadIdx.x >> 6) & 1, steps = span / 64;
+  if (operand) {  // rank tiles of 16, steps of 64 along K, 128 chunks of eight k each
+    const int x0 = 16 * (l >> 4) + 8 * h, all = (r + 15) / 16 * steps;
+    for (int q = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 7); q < all; q += WG / 128) {
+      const int jt = q / steps, st = q - jt * steps, j = 16 * jt + (l & 15);
+      const uint4 v = gather8<false>(s, ld, 64 * st + x0, j, j < r ? 8 : 0);
+      stg(operand + ((((long)jt * (K / 64) + first / 64 + st) * 2 + h) * 64 + l) * 8, v);
     }
   }
-  if (rows) {     // rows of ranks, padded to a multiple of 8
-    const int r8 = (r + 7) / 8, chunks = span * r8;
-    for (int q = threadIdx.x; q < chunks; q += 256) {
-      const int x = q / r8, j = 8 * (q - x * r8), n = r - j;
-      const uint4 v = RANKS_ALONG ? gather8<true>(s, ld, x, j, n) : gather8<false>(s, ld, j, x, n);
-      *reinterpret_cast<uint4*>(rows + ((long)(first + x) * r8 * 8 + j)) = v;
+  if (rows) {
+    const int r8 = (r + 7) / 8, inv = (1 << 16) / r8 + 1;  // q / r8 = q inv >> 16 for q < 2048
+    for (int q = threadIdx.x; q < span * r8; q += WG) {
+      const int x = q * inv >> 16, j = 8 * (q - x * r8);
+      stg(rows + ((long)(first + x) * r8 * 8 + j), gather8<true>(s, ld, x, j, r - j));
     }
   }
 }
 
-template <bool BITS8>
-__global__ __launch_bounds__(256) void k_adamw(AdamWParams p) {
-  __shared__ uint16_t s[ADAMW_LDS];
-  const lora_adamw_tile tile = p.tiles[blockIdx.x];
-  const lora_adamw_tensor t = p.tensors[tile.tensor];
-  const float* c = p.coef + (long)t.group * ADAMW_COEF;
-  if (c[C_ON] == 0.f) return;
-  const Place at = place(t, tile.first);
-  // the tile in LDS: its rows are the tensor's, of an odd length (columns are read too)
-  const int ld = (t.kind == KIND_A ? t.cols : 4 * at.len4) | 1;
+// The tile of B ([j][n], columns first .. of N) in Bop's order, and as B^T in rows of ranks.
+template <int WG>
+__device__ __forceinline__ void write_packs_b(const uint16_t* s, int ld, int r, int first, int span, int N, uint16_t* operand,
+                                              uint16_t* rows) {
+  const int l = threadIdx.x & 63, h = (threadIdx.x >> 6) & 1, steps = span / 64;
+  if (operand) {
+    const int x0 = 16 * (l >> 4) + 8 * h, all = (r + 15) / 16 * steps;
+    for (int q = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 7); q < all; q += WG / 128) {
+      const int jt = q / steps, st = q - jt * steps, j = 16 * jt + (l & 15);
+      uint4 v = zero4();
+      if (j < r) v = *reinterpret_cast<const uint4*>(s + j * ld + 64 * st + x0);
+      stg(operand + ((((long)jt * (N / 64) + first / 64 + st) * 2 + h) * 64 + l) * 8, v);
+    }
+  }
+  if (rows) {
+    const int r8 = (r + 7) / 8, inv = (1 << 16) / r8 + 1;
+    for (int q = threadIdx.x; q < span * r8; q += WG) {
+      const int x = q * inv >> 16, j = 8 * (q - x * r8);
+      stg(rows + ((long)(first + x) * r8 * 8 + j), gather8<false>(s, ld, j, x, r - j));
+    }
+  }
+}
+
+// The update of a tile in the registers of WG threads, and its bf16 form into LDS.  PART: the tile is the
+// end of a vector of no whole number of quads.
+template <bool BITS8, bool CLIP, bool PAST, int WG, bool PART, typename GetCoef>
+__device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& at, uint16_t* s, int ld, bool pack_a, bool pack_b,
+                                       GetCoef&& get_coef) {
+  constexpr int Q = ADAMW_TILE / 4 / WG;
+  float4 g4[Q], p4[Q], m4[Q], v4[Q];
+  uint32_t mc[Q], vc[Q];
+  float ms[Q], vs[Q];
+  // all loads first; a lane without a quad reads the tile's first, since a load under a condition would
+  // wait for those before it
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    const int i = threadIdx.x + WG * k, n = i < at.n4 ? at.n - 4 * i : PART ? 0 : 4;
+    const long o = at.at(i < at.n4 ? i : 0);
+    if (BITS8) {
+      mc[k] = ld4<PART, false>(reinterpret_cast<const uint8_t*>(t.m) + o, n);
+      vc[k] = ld4<PART, false>(reinterpret_cast<const uint8_t*>(t.v) + o, n);
+      ms[k] = ldg<float>(t.m_scale + o / ADAMW_BLOCK);
+      vs[k] = ldg<float>(t.v_scale + o / ADAMW_BLOCK);
+    } else {
+      m4[k] = ld4<PART, PAST>(reinterpret_cast<const float*>(t.m) + o, n);
+      v4[k] = ld4<PART, PAST>(reinterpret_cast<const float*>(t.v) + o, n);
+    }
+    g4[k] = ld4<PART, false>(t.grad + o, n);
+    p4[k] = ld4<PART, PAST>(t.param + o, n);
+  }
+  const Coef c = get_coef();
+  const bool quads = t.cols % 4 == 0;
+  const unsigned by_rank = (1u << 20) / (unsigned)max(1, min(t.cols, 64)) + 1;  // i / r of A, for i < 4096
 
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = threadIdx.x + 256 * k, n = at.n - 4 * i;
+  for (int k = 0; k < Q; ++k) {
+    const int i = threadIdx.x + WG * k, n = at.n - 4 * i;
+    if (Q > 1 && 4 * WG * k >= at.n) break;
     const bool live = i < at.n4;
-    int row = 0;
-    const long o = live ? at.at(i, row) : 0;
-    float4 g4 = make_float4(0.f, 0.f, 0.f, 0.f), p4 = g4, m4 = g4, v4 = g4;
-    uint32_t mc = 0, vc = 0;
-    float ms = 0.f, vs = 0.f;
-    if (live) {
-      g4 = ld4(t.grad + o, n);
-      p4 = ld4(t.param + o, n);
-      if (BITS8) {
-        mc = ld4(reinterpret_cast<const uint8_t*>(t.m) + o, n);
-        vc = ld4(reinterpret_cast<const uint8_t*>(t.v) + o, n);
-        ms = t.m_scale[o / ADAMW_BLOCK];
-        vs = t.v_scale[o / ADAMW_BLOCK];
-      } else {
-        m4 = ld4(reinterpret_cast<const float*>(t.m) + o, n);
-        v4 = ld4(reinterpret_cast<const float*>(t.v) + o, n);
-      }
-    }
-    float g[4] = {g4.x, g4.y, g4.z, g4.w}, w[4] = {p4.x, p4.y, p4.z, p4.w};
-    float m[4] = {m4.x, m4.y, m4.z, m4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w}, root[4];
+    const long o = at.at(i);
+    const float g[4] = {g4[k].x, g4[k].y, g4[k].z, g4[k].w};
+    float w[4] = {p4[k].x, p4[k].y, p4[k].z, p4[k].w};
+    float m[4], v[4], root[4];
     if (BITS8) {
-      values(mc, ms, m);
-      values(vc, vs, v);
+      values(mc[k], ms[k], m);
+      values(vc[k], vs[k], v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = v[e] * v[e];
+    } else {
+      m[0] = m4[k].x; m[1] = m4[k].y; m[2] = m4[k].z; m[3] = m4[k].w;
+      v[0] = v4[k].x; v[1] = v4[k].y; v[2] = v4[k].z; v[3] = v4[k].w;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float ge = p.norm ? g[e] * c[C_CLIP] : g[e];
-      m[e] = m[e] * c[C_B1] + ge * c[C_NB1];
-      v[e] = v[e] * c[C_B2] + (ge * ge) * c[C_NB2];
+      const float ge = CLIP ? g[e] * c.clip : g[e];
+      m[e] = m[e] * c.b1 + ge * c.nb1;
+      v[e] = v[e] * c.b2 + (ge * ge) * c.nb2;
       root[e] = sqrtf(v[e]);
-      w[e] = w[e] * c[C_KEEP] - (m[e] / (root[e] * c[C_ROOT] + c[C_EPS])) * c[C_RATE];
+      w[e] = w[e] * c.keep - (m[e] / (root[e] * c.root + c.eps)) * c.rate;
     }
     if (BITS8) {
-      float si, inv;
-      block_scale(m, si, inv);
-      float q[4];
+      if (PART) {  // a vector's end: what lies behind it is nothing to its block
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e >= n) m[e] = root[e] = 0.f;
+      }
+      float sm, sv, inv, q[4];
+      block_scale(m, sm, inv);
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[e] = m[e] * inv;
-      if (live) {
-        st4(reinterpret_cast<uint8_t*>(t.m) + o, codes(q), n);
-        if ((threadIdx.x & 15) == 0) t.m_scale[o / ADAMW_BLOCK] = si;
-      }
-      block_scale(root, si, inv);
+      const uint32_t cm = codes(q);
+      block_scale(root, sv, inv);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         q[e] = root[e] * inv;
         if (root[e] > 0.f && inv > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);  // the least code that is not 0
       }
-      if (live) {
-        st4(reinterpret_cast<uint8_t*>(t.v) + o, codes(q), n);
-        if ((threadIdx.x & 15) == 0) t.v_scale[o / ADAMW_BLOCK] = si;
+      if (!live) continue;
+      st4<PART, false>(reinterpret_cast<uint8_t*>(t.m) + o, cm, n);
+      st4<PART, false>(reinterpret_cast<uint8_t*>(t.v) + o, codes(q), n);
+      if ((threadIdx.x & 15) == 0) {
+        stg(t.m_scale + o / ADAMW_BLOCK, sm);
+        stg(t.v_scale + o / ADAMW_BLOCK, sv);
       }
-    } else if (live) {
-      st4(reinterpret_cast<float*>(t.m) + o, make_float4(m[0], m[1], m[2], m[3]), n);
-      st4(reinterpret_cast<float*>(t.v) + o, make_float4(v[0], v[1], v[2], v[3]), n);
+    } else {
+      if (!live) continue;
+      st4<PART, PAST>(reinterpret_cast<float*>(t.m) + o, m, n);
+      st4<PART, PAST>(reinterpret_cast<float*>(t.v) + o, v, n);
     }
-    if (!live) continue;
-    st4(t.param + o, make_float4(w[0], w[1], w[2], w[3]), n);
-    if (t.copy || t.kind != KIND_PLAIN) {
-      const uint32_t lo = bf16x2_rne(w[0], w[1]), hi = bf16x2_rne(w[2], w[3]);
-      if (t.copy) {
-        if (n >= 4) {
-          *reinterpret_cast<uint2*>(t.copy + o) = make_uint2(lo, hi);
-        } else {
-          t.copy[o] = (uint16_t)lo;
-          if (n > 1) t.copy[o + 1] = (uint16_t)(lo >> 16);
-          if (n > 2) t.copy[o + 2] = (uint16_t)hi;
-        }
-      }
-      const uint16_t b[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-      if (t.kind == KIND_A) {
-        int k0 = 4 * i / t.cols, j = 4 * i - k0 * t.cols;
+    st4<PART, PAST>(t.param + o, w, n);
+    const uint2 b = make_uint2(bf16x2_rne(w[0], w[1]), bf16x2_rne(w[2], w[3]));
+    if (t.copy) st4<PART>(t.copy + o, b, n);
+    if (PART) continue;
+    if (pack_a) {
+      if (t.pack_bwd && t.cols % 8 == 0) stg(t.pack_bwd + o, b);  // rows without padding
+      int k0 = (int)((unsigned)(4 * i) * by_rank >> 20), j = 4 * i - k0 * t.cols;
+      if (quads) {
+        *reinterpret_cast<uint2*>(s + k0 * ld + j) = b;
+      } else {
+        const uint16_t each[4] = {(uint16_t)b.x, (uint16_t)(b.x >> 16), (uint16_t)b.y, (uint16_t)(b.y >> 16)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[k0 * ld + j] = b[e];
+          s[k0 * ld + j] = each[e];
           if (++j == t.cols) { j = 0; ++k0; }
         }
-      } else if (t.kind == KIND_B) {
-        const int x = row * ld + 4 * (i - row * at.len4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x + e] = b[e];
       }
+    } else if (pack_b) {
+      const int row = at.row(i);
+      *reinterpret_cast<uint2*>(s + row * ld + 4 * (i - row * at.len4)) = b;
     }
   }
-  if (t.kind == KIND_PLAIN || (!t.pack && !t.pack_bwd)) return;
-  __syncthreads();
-  if (t.kind == KIND_A) write_packs<true>(s, ld, t.cols, tile.first, at.n / t.cols, t.rows, t.pack, t.pack_bwd);
-  else write_packs<false>(s, ld, t.rows, tile.first, 4 * at.len4, t.cols, t.pack_bwd, t.pack);
+}
+
+// A workgroup a tile.  ALONE: the launch is the whole step (no norms, few tiles): every workgroup works
+// out its group's coefficients while its loads are in flight, and the group's last counts its step.
+template <bool BITS8, bool CLIP, bool ALONE, bool PAST, int WG>
+__global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
+  __shared__ __attribute__((aligned(16))) uint16_t s[ADAMW_LDS];
+  const lora_adamw_tile tile = p.tiles[blockIdx.x];
+  const lora_adamw_tensor& t = tile.tensor;
+  // the whole record is here before anything is decided by it: read field by field where each is
+  // needed, it costs a round of latency each
+  asm volatile("" ::"s"(t.param), "s"(t.grad), "s"(t.m), "s"(t.v), "s"(t.m_scale), "s"(t.v_scale), "s"(t.copy), "s"(t.pack),
+               "s"(t.pack_bwd), "s"(t.rows), "s"(t.cols), "s"(t.group), "s"(t.kind), "s"(tile.first));
+  c_float* cp = (c_float*)(reinterpret_cast<uintptr_t>(p.coef) + (size_t)t.group * ADAMW_COEF * sizeof(float));
+  if (ALONE ? p.active && !p.active[t.group] : cp[9] == 0.f) return;
+  const Place at = place(t, tile.first);
+  // The tile in LDS: A's rows padded so that eight rows' columns lie in other banks (by 4 where a quad
+  // lies in one row, and else to an odd length), B's by 8, which keeps its 16-byte pieces aligned.
+  const bool pack_a = t.kind == KIND_A && (t.pack || t.pack_bwd), pack_b = t.kind == KIND_B && (t.pack || t.pack_bwd);
+  const int ld = t.kind == KIND_A ? (t.cols % 4 == 0 ? t.cols + 4 : t.cols | 1) : 4 * at.len4 + 8;
+  int step = 0;
+  auto coef = [&]() {
+    if (!ALONE) return get(cp);
+    step = p.steps[t.group] + 1;
+    return coefficients(p.hyper + (long)t.group * ADAMW_HYPER, step, 1.0);
+  };
+  if (at.n & 3) update<BITS8, CLIP, PAST, WG, true>(t, at, s, ld, pack_a, pack_b, coef);
+  else update<BITS8, CLIP, PAST, WG, false>(t, at, s, ld, pack_a, pack_b, coef);
+  if (ALONE || pack_a || pack_b) __syncthreads();
+  if (ALONE && threadIdx.x == 0) {
+    // every wave of this workgroup has read the group's step (its values depend on it)
+    if (add_agent(p.arrived + ADAMW_LINE * t.group, 1) == p.group_first[t.group + 1] - p.group_first[t.group] - 1) {
+      p.steps[t.group] = step;
+      set_agent(p.arrived + ADAMW_LINE * t.group, 0);
+    }
+  }
+  if (pack_a) write_packs_a<WG>(s, ld, t.cols, tile.first, at.n / t.cols, t.rows, t.pack, t.cols % 8 ? t.pack_bwd : nullptr);
+  if (pack_b) write_packs_b<WG>(s, ld, t.rows, tile.first, 4 * at.len4, t.cols, t.pack_bwd, t.pack);
+}
+
+// Steps of few tiles without norms are one launch.  More tiles than this and the arrivals at one
+// group's counter, one behind another, take longer than a launch for the groups.
+constexpr long ALONE_TILES = 256;
+
+// Steps of more tiles than this (8 million values, 250 MB and more) read and write their states and
+// master copies past the caches, which could not hold them until the next step: what the norms'
+// launch has read of the gradients then stays for the update.
+constexpr long STREAM_TILES = 2048;
+
+constexpr int WG = 1024;
+
+template <bool BITS8>
+void launch_update(const AdamWParams& p, bool alone, hipStream_t s) {
+  const dim3 grid((unsigned)p.n_tiles), wg(WG);
+  const bool past = p.n_tiles > STREAM_TILES;
+  if (alone) hipLaunchKernelGGL((k_adamw<BITS8, false, true, false, WG>), grid, wg, 0, s, p);
+  else if (p.norm && past) hipLaunchKernelGGL((k_adamw<BITS8, true, false, true, WG>), grid, wg, 0, s, p);
+  else if (p.norm) hipLaunchKernelGGL((k_adamw<BITS8, true, false, false, WG>), grid, wg, 0, s, p);
+  else if (past) hipLaunchKernelGGL((k_adamw<BITS8, false, false, true, WG>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_adamw<BITS8, false, false, false, WG>), grid, wg, 0, s, p);
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamWParams& p, int state_bits, hipStream_t s) {
-  if (p.norm && p.n_tiles) hipLaunchKernelGGL(k_adamw_norms, dim3((unsigned)p.n_tiles), dim3(256), 0, s, p);
-  hipLaunchKernelGGL(k_adamw_groups, dim3(p.n_groups), dim3(256), 0, s, p);
-  if (p.n_tiles) {
-    if (state_bits == 8) hipLaunchKernelGGL(k_adamw<true>, dim3((unsigned)p.n_tiles), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(k_adamw<false>, dim3((unsigned)p.n_tiles), dim3(256), 0, s, p);
-  }
+  const bool alone = !p.norm && p.n_tiles <= ALONE_TILES;
+  if (p.norm && p.n_tiles) hipLaunchKernelGGL(k_adamw_norms, dim3((unsigned)((p.n_tiles + 3) / 4)), dim3(256), 0, s, p);
+  if (!alone) hipLaunchKernelGGL(k_adamw_groups, dim3(p.n_groups), dim3(256), 0, s, p);
+  if (p.n_tiles == 0) return hipGetLastError();
+  if (state_bits == 8) launch_update<true>(p, alone, s);
+  else launch_update<false>(p, alone, s);
   return hipGetLastError();
 }
 

@@ -74,30 +74,29 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// table, tiles, group_first, state_bits, hyper, active, steps, clip, grad_norm, status, workspace, stream -> grad_norm or None
+// tiles, group_first, state_bits, hyper, active, steps, clip, grad_norm, status, workspace, stream -> grad_norm or None
 PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&]() -> PyObject* {
-    const Tensor &table = req(a[0], "table"), &tiles = req(a[1], "tiles"), &first = req(a[2], "group_first");
-    const at::Device dev = table.device();
+  return guarded(n, 11, [&]() -> PyObject* {
+    const Tensor &tiles = req(a[0], "tiles"), &first = req(a[1], "group_first");
+    const at::Device dev = tiles.device();
     const int64_t n_tiles = tiles.size(0);
     const int32_t G = tokens(first, "group_first") - 1;
-    const void* pt = need(table, "table", at::kByte, {table.numel()}, dev);
-    const void* pl = need(tiles, "tiles", at::kInt, {n_tiles, 2}, dev);
+    const void* pl = need(tiles, "tiles", at::kByte, {n_tiles, (int64_t)sizeof(lora_adamw_tile)}, dev);
     const void* pf = need(first, "group_first", at::kInt, {(int64_t)G + 1}, dev);
-    const void* ph = need(req(a[4], "hyper"), "hyper", at::kDouble, {G, 6}, dev);
-    const void* pa = need_or_null(opt(a[5], "active"), "active", at::kInt, {G}, dev);
-    void* ps = need(req(a[6], "steps"), "steps", at::kInt, {G}, dev);
-    const bool clip = truth(a[7], "clip");
-    const Tensor *on = opt(a[8], "grad_norm"), &ws = req(a[10], "workspace");
+    const void* ph = need(req(a[3], "hyper"), "hyper", at::kDouble, {G, 6}, dev);
+    const void* pa = need_or_null(opt(a[4], "active"), "active", at::kInt, {G}, dev);
+    void* ps = need(req(a[5], "steps"), "steps", at::kInt, {G}, dev);
+    const bool clip = truth(a[6], "clip");
+    const Tensor *on = opt(a[7], "grad_norm"), &ws = req(a[9], "workspace");
     if (on && !clip) throw Refused("grad_norm is for a step that clips");
     Tensor norm;
     if (clip) norm = on ? *on : empty({G}, at::kFloat, dev);
     void* pw = need(ws, "workspace", at::kByte, {ws.numel()}, dev);
     const lora_status s = lora_adamw_step(
-        static_cast<const lora_adamw_tensor*>(pt), static_cast<const lora_adamw_tile*>(pl), n_tiles, static_cast<const int32_t*>(pf),
-        G, int32(a[3]), static_cast<const double*>(ph), static_cast<const int32_t*>(pa), static_cast<int32_t*>(ps),
-        clip ? static_cast<float*>(need(norm, "grad_norm", at::kFloat, {G}, dev)) : nullptr, status_word(a[9], dev), pw,
-        (size_t)ws.numel(), stream(a[11]));
+        static_cast<const lora_adamw_tile*>(pl), n_tiles, static_cast<const int32_t*>(pf), G, int32(a[2]),
+        static_cast<const double*>(ph), static_cast<const int32_t*>(pa), static_cast<int32_t*>(ps),
+        clip ? static_cast<float*>(need(norm, "grad_norm", at::kFloat, {G}, dev)) : nullptr, status_word(a[8], dev), pw,
+        (size_t)ws.numel(), stream(a[10]));
     if (s != LORA_OK) return status(s);
     if (!clip) Py_RETURN_NONE;
     return THPVariable_Wrap(norm);

@@ -164,7 +164,7 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
     for (int32_t i = 0; i < n; ++i) {
       int64_t side, span;
       cut(tensors[i], side, span);
-      for (int64_t at = 0; at < side; at += span) tiles[first[tensors[i].group]++] = {i, (int32_t)at};
+      for (int64_t at = 0; at < side; at += span) tiles[first[tensors[i].group]++] = {tensors[i], (int32_t)at, 0};
     }
     return LORA_OK;
   } catch (const std::bad_alloc&) {
@@ -174,26 +174,27 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
 
 size_t lora_adamw_workspace_bytes(int64_t n_tiles, int32_t n_groups) {
   if (n_tiles < 0 || n_tiles > MAX_TILES || n_groups < 1 || n_groups > MAX_GROUPS) return 0;
-  return round256((size_t)n_tiles * sizeof(double)) + (size_t)n_groups * ADAMW_COEF * sizeof(float);
+  return round256((size_t)n_tiles * sizeof(double)) + round256((size_t)n_groups * ADAMW_COEF * sizeof(float)) +
+         (size_t)n_groups * ADAMW_LINE * sizeof(int);
 }
 
-lora_status lora_adamw_step(const lora_adamw_tensor* tensors, const lora_adamw_tile* tiles, int64_t n_tiles,
-                            const int32_t* group_first, int32_t n_groups, int32_t state_bits, const double* hyper,
-                            const int32_t* active, int32_t* steps, float* grad_norm, int32_t* status, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+lora_status lora_adamw_step(const lora_adamw_tile* tiles, int64_t n_tiles, const int32_t* group_first, int32_t n_groups,
+                            int32_t state_bits, const double* hyper, const int32_t* active, int32_t* steps,
+                            float* grad_norm, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
   if (n_tiles < 0 || n_groups < 1 || (state_bits != 32 && state_bits != 8)) return LORA_ERR_INVALID_ARG;
   if (n_tiles > MAX_TILES || n_groups > MAX_GROUPS) return LORA_ERR_UNSUPPORTED;
-  if ((n_tiles > 0 && (!tensors || !tiles)) || !aligned(tensors, 8) || !aligned(tiles, 8) || !group_first ||
+  if ((n_tiles > 0 && !tiles) || !aligned(tiles, 8) || !group_first ||
       !aligned(group_first, 4) || !hyper || !aligned(hyper, 8) || !aligned(active, 4) || !steps || !aligned(steps, 4) ||
       !aligned(grad_norm, 4) || !aligned(status, 4))
     return LORA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_adamw_workspace_bytes(n_tiles, n_groups))
     return LORA_ERR_WORKSPACE;
   AdamWParams p{};
-  p.tensors = tensors; p.tiles = tiles; p.n_tiles = n_tiles; p.group_first = group_first; p.n_groups = n_groups;
+  p.tiles = tiles; p.n_tiles = n_tiles; p.group_first = group_first; p.n_groups = n_groups;
   p.hyper = hyper; p.active = active; p.steps = steps; p.norm = grad_norm; p.status = status;
   p.part = reinterpret_cast<double*>(workspace);
   p.coef = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + round256((size_t)n_tiles * sizeof(double)));
+  p.arrived = reinterpret_cast<int*>(reinterpret_cast<char*>(p.coef) + round256((size_t)n_groups * ADAMW_COEF * sizeof(float)));
   return launch_adamw(p, state_bits, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 

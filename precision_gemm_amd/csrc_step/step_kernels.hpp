@@ -47,7 +47,6 @@ constexpr int NORM_BWD_WGS = 256;  // most workgroups of the backward (one a CU)
 
 // An AdamW step over many tensors.
 struct AdamWParams {
-  const lora_adamw_tensor* tensors;
   const lora_adamw_tile* tiles;
   long n_tiles;
   const int* group_first;    // [n_groups + 1]: the groups' tiles
@@ -59,15 +58,19 @@ struct AdamWParams {
   int* status;
   double* part;              // [n_tiles]: sums of squares
   float* coef;               // [n_groups][ADAMW_COEF]
+  int* arrived;              // [n_groups][ADAMW_LINE]: tiles of the group that are done; 0 between calls
 };
 
 constexpr int ADAMW_HYPER = 6;   // rate, beta1, beta2, eps, weight decay, largest norm
 constexpr int ADAMW_COEF = 12;
+constexpr int ADAMW_LINE = 32;   // words of a cache line: each group's arrivals on a line of their own
 constexpr int ADAMW_TILE = 4096; // most values of a tile
 constexpr int ADAMW_BLOCK = 64;  // values that share a scale of the 8-bit states
 
-// Rows of A (columns of B) that a tile takes, for rank r.
-inline __host__ __device__ int adamw_tile_span(int r) { return 64 * (64 / r > 1 ? 64 / r : 1); }
+// Rows of A (columns of B) that a tile takes, for rank r: 4,096 values for ranks of 16, 32 and 64.  Small
+// ranks write more padding than values, and tiles of 4,096 of them take longer than they save (rank 8,
+// one adapter of 4096 x 4096: 512 rows 6.2 us, 256 rows 5.4).
+inline __host__ __device__ int adamw_tile_span(int r) { return r <= 4 ? 512 : r <= 16 ? 256 : r <= 32 ? 128 : 64; }
 
 hipError_t launch_adamw(const AdamWParams& p, int state_bits, hipStream_t s);
 

@@ -90,17 +90,16 @@ class AdamW:
         plan = lambda tiles, first: check("lora_adamw_plan", lib().lora_adamw_plan(  # noqa: E731
             structs, len(self.tensors), self.n_groups, state_bits, ctypes.byref(n_tiles), tiles, first))
         plan(None, None)
-        tiles = np.zeros((n_tiles.value, 2), np.int32)
+        tiles = np.zeros((n_tiles.value, ctypes.sizeof(AdamWTensorStruct) + 8), np.uint8)
         first = np.zeros(self.n_groups + 1, np.int32)
         plan(tiles.ctypes.data_as(ctypes.c_void_p), first.ctypes.data_as(ctypes.c_void_p))
         up = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
-        self.table = up(np.frombuffer(structs, np.uint8).copy())
         self.tiles, self.group_first = up(tiles), up(first)
         if steps is None:
             steps = torch.zeros(self.n_groups, dtype=torch.int32, device=dev)
         _check(steps, "steps", torch.int32, self.n_groups, dev)
         self.steps = steps
-        self.workspace = torch.empty(max(16, int(lib().lora_adamw_workspace_bytes(n_tiles.value, self.n_groups))),
+        self.workspace = torch.zeros(max(16, int(lib().lora_adamw_workspace_bytes(n_tiles.value, self.n_groups))),
                                      dtype=torch.uint8, device=dev)
 
     def _fill(self, t: AdamWTensor, s, dev) -> None:
@@ -154,5 +153,5 @@ def adamw_step(opt: AdamW, hyper: torch.Tensor, *, active: torch.Tensor | None =
     it was (LORA_ADAMW_NOT_FINITE in ``status``, int32 [1]), and the norms are returned, float32
     [n_groups] (in ``grad_norm`` if given); without it gradients are taken as they are, and None is
     returned.  Apart from the norms the call allocates nothing, and can be captured in a HIP graph."""
-    return call("adamw_step", opt.table, opt.table, opt.tiles, opt.group_first, opt.state_bits, hyper, active, opt.steps, clip,
+    return call("adamw_step", opt.tiles, opt.tiles, opt.group_first, opt.state_bits, hyper, active, opt.steps, clip,
                 grad_norm, status, opt.workspace)

@@ -88,14 +88,18 @@ def tensor(rows, cols, kind, group=0, bits=32, at=None, **kw):
     return s
 
 
+class Tile(ctypes.Structure):
+    _fields_ = [("tensor", AdamWTensorStruct), ("first", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def plan(L, tensors, n_groups=2, bits=32, want=True):
     a = (AdamWTensorStruct * max(1, len(tensors)))(*tensors)
     n = ctypes.c_int64(-5)
     st = L.lora_adamw_plan(a, len(tensors), n_groups, bits, ctypes.byref(n), None, None)
     if st != OK or not want:
         return st, n.value, None, None
-    tiles, first = np.full((n.value, 2), -1, np.int32), np.full(n_groups + 1, -1, np.int32)
-    st = L.lora_adamw_plan(a, len(tensors), n_groups, bits, ctypes.byref(n), tiles.ctypes.data, first.ctypes.data)
+    tiles, first = (Tile * n.value)(), np.full(n_groups + 1, -1, np.int32)
+    st = L.lora_adamw_plan(a, len(tensors), n_groups, bits, ctypes.byref(n), tiles, first.ctypes.data)
     return st, n.value, tiles, first
 
 
@@ -108,13 +112,15 @@ def test_plan_covers_every_value_once(L):
     st, n, tiles, first = plan(L, ts, n_groups=4)
     assert st == OK and n == len(tiles) == first[4] and first[0] == 0 and first[3] == first[4]
     for g in range(4):
-        for i, f in tiles[first[g]:first[g + 1]]:
-            assert ts[i].group == g
-    for i, t in enumerate(ts):
-        starts = sorted(f for j, f in tiles if j == i)
+        for x in tiles[first[g]:first[g + 1]]:
+            assert x.tensor.group == g
+    for t in ts:
+        mine = [x for x in tiles if x.tensor.param == t.param]
+        assert all(bytes(x.tensor) == bytes(t) for x in mine)
+        starts = sorted(x.first for x in mine)
         side = t.rows if t.kind == 1 else t.cols if t.kind == 2 else t.rows * t.cols
         r = t.cols if t.kind == 1 else t.rows
-        span = 4096 if t.kind == 0 else 64 * max(1, 64 // r)
+        span = 4096 if t.kind == 0 else 512 if r <= 4 else 256 if r <= 16 else 128 if r <= 32 else 64
         assert starts == list(range(0, side, span))
 
 
@@ -143,11 +149,11 @@ def test_plan_refuses_more(L):
     n = ctypes.c_int64(0)
     assert L.lora_adamw_plan(None, 1, 1, 32, ctypes.byref(n), None, None) == INVALID
     assert L.lora_adamw_plan(None, 0, 1, 32, ctypes.byref(n), None, None) == OK and n.value == 0
-    a, tiles, first = (AdamWTensorStruct * 1)(tensor(1, 64, 0)), np.zeros((9, 2), np.int32), np.zeros(2, np.int32)
+    a, tiles, first = (AdamWTensorStruct * 1)(tensor(1, 64, 0)), (Tile * 9)(), np.zeros(2, np.int32)
     n.value = 9  # not the number of tiles
-    assert L.lora_adamw_plan(a, 1, 1, 32, ctypes.byref(n), tiles.ctypes.data, first.ctypes.data) == INVALID
+    assert L.lora_adamw_plan(a, 1, 1, 32, ctypes.byref(n), tiles, first.ctypes.data) == INVALID
     n.value = 1
-    assert L.lora_adamw_plan(a, 1, 1, 32, ctypes.byref(n), tiles.ctypes.data, None) == INVALID
+    assert L.lora_adamw_plan(a, 1, 1, 32, ctypes.byref(n), tiles, None) == INVALID
 
 
 def test_plan_refuses_overlaps(L):
@@ -169,13 +175,13 @@ def test_plan_refuses_overlaps(L):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(), WORKSPACE), (dict(ws=ODD, wsb=1 << 20), WORKSPACE), (dict(ws=FAKE, wsb=64), WORKSPACE), (dict(n=-1), INVALID),
-    (dict(n=1 << 31), UNSUPPORTED), (dict(G=0), INVALID), (dict(G=9000), UNSUPPORTED), (dict(bits=16), INVALID), (dict(t=NULL), INVALID),
+    (dict(n=1 << 31), UNSUPPORTED), (dict(G=0), INVALID), (dict(G=9000), UNSUPPORTED), (dict(bits=16), INVALID),
     (dict(tiles=NULL), INVALID), (dict(first=NULL), INVALID), (dict(hyper=NULL), INVALID), (dict(hyper=ctypes.c_void_p(0x1004)), INVALID),
     (dict(steps=NULL), INVALID), (dict(active=ctypes.c_void_p(0x1002)), INVALID), (dict(norm=ctypes.c_void_p(0x1002)), INVALID)])
 def test_step(L, kw, status):
-    base = dict(t=FAKE, tiles=FAKE, n=5, first=FAKE, G=2, bits=32, hyper=FAKE, active=FAKE, steps=FAKE, norm=FAKE, st=NULL, ws=NULL,
+    base = dict(tiles=FAKE, n=5, first=FAKE, G=2, bits=32, hyper=FAKE, active=FAKE, steps=FAKE, norm=FAKE, st=NULL, ws=NULL,
                 wsb=0, stream=NULL)
-    assert call(L.lora_adamw_step, "t tiles n first G bits hyper active steps norm st ws wsb stream", base, **kw) == status
+    assert call(L.lora_adamw_step, "tiles n first G bits hyper active steps norm st ws wsb stream", base, **kw) == status
 
 
 def test_step_workspace_bytes(L):
