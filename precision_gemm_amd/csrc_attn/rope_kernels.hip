@@ -19,6 +19,7 @@
 
 #include "attn_kernels.hpp"
 #include "../csrc/device_common.hpp"
+#include "row_buffer.hpp"
 
 namespace lora {
 namespace {
@@ -267,37 +268,27 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
   const int all = p.T * rounds;
   const int first = (int)((long)all * at / n_waves), last = (int)((long)all * (at + 1) / n_waves);
 
-  // a (token, round): heads h of this lane's slot, places of its gradient, input and result
+  // a (token, round): heads h of this lane's slot, places of its gradient, input and result.  Heads
+  // behind the last, and values without dv, are outside their rows' buffers.
   struct Round { uint4 ga, gb, xa, xb; };
-  auto head = [&](int r, bool& value, bool& live) {
+  auto head = [&](int r, bool& value) {
     value = kv && r >= p.rounds_k;
-    const int h = (value ? r - p.rounds_k : r) * SLOTS + sl;
-    live = h < (kv ? p.n_kv : p.n_q) && !(value && !p.dv);
-    return h;
+    return (value ? r - p.rounds_k : r) * SLOTS + sl;
   };
-  auto load = [&](int t, int r) {
-    bool value, live;
-    const int h = head(r, value, live);
-    const uint16_t* g = (kv ? (value ? p.dv : p.dk) + ((long)t * p.n_kv + h) * D : p.dq + ((long)t * p.n_q + h) * D);
-    const uint16_t* x = p.qkv + (long)t * p.ld + (long)(h + (kv ? p.n_q : 0)) * D;
-    Round v{zero4(), zero4(), zero4(), zero4()};
-    if (live) {
-      v.ga = ldg16(g + m.a);
-      v.gb = ldg16(g + m.b);
-      if (w && !value) {
-        v.xa = ldg16(x + m.a);
-        v.xb = ldg16(x + m.b);
-      }
-    }
-    return v;
+  const int n_heads = kv ? p.n_kv : p.n_q;
+  auto load = [&](int t, int r, bool there) {
+    bool value;
+    const int at = head(r, value) * D;
+    const RowBuffer g(kv ? (value ? p.dv : p.dk) : p.dq, (long)n_heads * D, t, n_heads * D, there && !(value && !p.dv));
+    const RowBuffer x(p.qkv + (kv ? (long)p.n_q * D : 0), p.ld, t, n_heads * D, there && w && !value);
+    return Round{g.load(at + m.a), g.load(at + m.b), x.load(at + m.a), x.load(at + m.b)};
   };
 
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
   int t = first / rounds, r = first - t * rounds;
-  Round next{};
-  if (first < last) next = load(t, r);
+  Round next = load(t, r, first < last);
   bool placed = true, fresh = true;
   Turn tn;
   for (int it = first; it < last; ++it) {
@@ -314,16 +305,16 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
       r = 0;
       ++t;
     }
-    if (it + 1 < last) next = load(t, r);
+    next = load(t, r, it + 1 < last);
 
-    bool value, live;
-    const int h = head(r0, value, live);
-    uint16_t* dst = p.dqkv + (long)t0 * p.ldd + (long)(h + (kv ? (value ? p.n_q + p.n_kv : p.n_q) : 0)) * D;
+    bool value;
+    const int h = head(r0, value);
+    const bool live = h < n_heads;
+    const RowBuffer dst(p.dqkv + (long)(kv ? (value ? p.n_q + p.n_kv : p.n_q) : 0) * D, p.ldd, t0, n_heads * D,
+                        !(value && !p.dv));
     if (value) {  // values pass through
-      if (live) {
-        *reinterpret_cast<uint4*>(dst + m.a) = now.ga;
-        *reinterpret_cast<uint4*>(dst + m.b) = now.gb;
-      }
+      dst.store(h * D + m.a, now.ga);
+      dst.store(h * D + m.b, now.gb);
       continue;
     }
     float g[16];
@@ -357,10 +348,8 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) g[e] = rs * (g[e] - x[e] * mean);
     }
-    if (live) {
-      *reinterpret_cast<uint4*>(dst + m.a) = placed ? narrow(g) : zero4();
-      *reinterpret_cast<uint4*>(dst + m.b) = placed ? narrow(g + 8) : zero4();
-    }
+    dst.store(h * D + m.a, placed ? narrow(g) : zero4());
+    dst.store(h * D + m.b, placed ? narrow(g + 8) : zero4());
   }
   if (!w) return;
   float* row = red[wave * SLOTS + sl];

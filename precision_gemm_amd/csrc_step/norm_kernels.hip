@@ -10,6 +10,7 @@
 
 #include "step_kernels.hpp"
 #include "../csrc/device_common.hpp"
+#include "../csrc_attn/row_buffer.hpp"
 
 namespace lora {
 namespace {
@@ -26,8 +27,17 @@ __device__ __forceinline__ void ld8(const float* p, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// The compiler takes the value as new from here on.
-__device__ __forceinline__ void opaque(uint4& v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+// s plus the sum of eight bf16: two products by 1 an instruction, exact, added in fp32.
+__device__ __forceinline__ float sum8(const uint4& v, float s) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const bf16x2 one = __builtin_bit_cast(bf16x2, 0x3f803f80u);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v.x), one, s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v.y), one, s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v.z), one, s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v.w), one, s, false);
+#endif
+  return s;
+}
 
 // Sum over a wave, the same in every lane: four steps within rows of 16 lanes, two across them,
 // on the DPP path (no LDS).
@@ -67,35 +77,33 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*slot)[N]) {
 }
 
 // TPR threads a row, C chunks of 8 values a thread, WG threads a workgroup.
-template <int TPR, int C, int WG, bool RMS>
+template <int TPR, int C, int WG, bool RMS, bool RES>
 __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
   constexpr int WAVES = TPR / 64;
   __shared__ float red[2][WG / 64][1];
   const int tid = threadIdx.x % TPR;
-  const int t = blockIdx.x * (WG / TPR) + threadIdx.x / TPR;
+  const int t = blockIdx.x * (WG / TPR) + __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const bool row = t < p.T;
+  const RowBuffer rx(p.x, p.ldx, t, p.K, row), ry(p.y, p.ldy, t, p.K, row);
+  const RowBuffer rr(p.residual, p.ldr, t, p.K, RES && row), rs(p.sum, p.lds, t, p.K, RES && row);
+  uint4 x[C], res[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c] = rx.load((c * TPR + tid) * 8);
+  if (RES) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) res[c] = rr.load((c * TPR + tid) * 8);
+  }
   float h[C][8];
-  bool live[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * TPR + tid) * 8;
-    live[c] = row && col < p.K;
-    uint4 a = zero4();
-    if (live[c]) a = ldg16(p.x + (long)t * p.ldx + col);
-    widen(a, h[c]);
-  }
-  if (p.residual) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * TPR + tid) * 8;
-      uint4 a = zero4();
-      if (live[c]) a = ldg16(p.residual + (long)t * p.ldr + col);
+    widen(x[c], h[c]);
+    if (RES) {
       float r[8];
-      widen(a, r);
+      widen(res[c], r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[e] += h[c][e];
-      a = narrow(r);  // the stream's own rounding: the statistics are those of what is stored
-      if (live[c]) *reinterpret_cast<uint4*>(p.sum + (long)t * p.lds + col) = a;
+      const uint4 a = narrow(r);  // the stream's own rounding: the statistics are those of what is stored
+      rs.store((c * TPR + tid) * 8, a);
       widen(a, h[c]);
     }
   }
@@ -111,21 +119,23 @@ __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
   }
   float q[1] = {0.f};
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    float part = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       h[c][e] -= mean;
-      q[0] += live[c] ? h[c][e] * h[c][e] : 0.f;
+      part += h[c][e] * h[c][e];
     }
+    q[0] += (c * TPR + tid) * 8 < p.K ? part : 0.f;
+  }
   row_sum<WAVES, 1>(q, red[1]);
   const float r = 1.0f / sqrtf(q[0] / (float)p.K + p.eps);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * TPR + tid) * 8;
-    if (!live[c]) continue;
     float w[8], b[8];
-    if (p.weight) ld8(p.weight + col, w);
-    if (p.bias) ld8(p.bias + col, b);
+    if (p.weight && col < p.K) ld8(p.weight + col, w);
+    if (p.bias && col < p.K) ld8(p.bias + col, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float v = h[c][e] * r;
@@ -133,115 +143,119 @@ __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
       if (p.bias) v += b[e];
       h[c][e] = v;
     }
-    *reinterpret_cast<uint4*>(p.y + (long)t * p.ldy + col) = narrow(h[c]);
+    ry.store(col, narrow(h[c]));
   }
 }
 
-// Backward.  A workgroup takes rows blockIdx.x * (WG / TPR) + ... in strides of the grid; a
-// thread meets the same columns in every row, so it keeps their sums for the weights' gradients
-// in registers.
-template <int TPR, int C, int WG, bool AHEAD, bool RMS>
+// Backward.  A workgroup takes rows blockIdx.x * (WG / TPR) + ... in strides of the grid, the loads of
+// the next AHEAD of them in flight; a thread meets the same columns in every row, so it keeps their
+// weights, and their sums for the weights' gradients, in registers.
+template <int TPR, int C, int WG, int AHEAD, bool RMS, bool DSUM>
 __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
   constexpr int WAVES = TPR / 64, ROWS = WG / TPR;
   __shared__ float red0[WG / 64][1], red1[WG / 64][1], red2[WG / 64][2];
   __shared__ __attribute__((aligned(16))) float join[ROWS > 1 ? (ROWS - 1) * TPR * C * 8 : 4];
-  const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const int tid = threadIdx.x % TPR, group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const float inv = 1.0f / (float)p.K;
-  float dw[C][8], db[C][8];
+  float dw[C][8], db[C][8], w[C][8];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[c][e] = db[c][e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      dw[c][e] = db[c][e] = 0.f;
+      w[c][e] = 1.f;
+    }
+    if (p.weight && (c * TPR + tid) * 8 < p.K) ld8(p.weight + (c * TPR + tid) * 8, w[c]);
+  }
 
+  // four chunks a thread leave no registers for the residual stream's gradient ahead of its row
+  constexpr bool SUM_AHEAD = DSUM && C * WG <= 1024;
   struct Row { uint4 h[C], g[C], s[C]; };
+  auto load_sum = [&](int t, Row& v) {
+    const RowBuffer rs(p.dsum, p.ldds, t, p.K, t < p.T);
+#pragma unroll
+    for (int c = 0; c < C; ++c) v.s[c] = rs.load((c * TPR + tid) * 8);
+  };
   auto load = [&](int t) {
+    const RowBuffer rh(p.h, p.ldh, t, p.K, t < p.T), rg(p.dy, p.lddy, t, p.K, t < p.T);
     Row v;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * TPR + tid) * 8;
-      v.h[c] = v.g[c] = v.s[c] = zero4();
-      if (t < p.T && col < p.K) {
-        v.h[c] = ldg16(p.h + (long)t * p.ldh + col);
-        v.g[c] = ldg16(p.dy + (long)t * p.lddy + col);
-        if (p.dsum) v.s[c] = ldg16(p.dsum + (long)t * p.ldds + col);
-      }
+      v.h[c] = rh.load(col);
+      v.g[c] = rg.load(col);
     }
+    if (SUM_AHEAD) load_sum(t, v);
     return v;
   };
-  Row next;
-  if (AHEAD) next = load(blockIdx.x * ROWS + group);
-  for (int t0 = blockIdx.x * ROWS; t0 < p.T; t0 += gridDim.x * ROWS) {
-    const int t = t0 + group;
-    Row now = AHEAD ? next : load(t);
-    if (AHEAD && t0 + (int)gridDim.x * ROWS < p.T) next = load(t + gridDim.x * ROWS);
-    // Each pass widens the row's bf16 anew (`opaque`): held in fp32 from pass to pass they would take
-    // the registers that the sums and the next row's loads need.
+  auto row = [&](int t, const Row& now) {
+    float h[C][8], g[C][8];  // h, then xh; dy, then g
+#pragma unroll
+    for (int c = 0; c < C; ++c) widen(now.h[c], h[c]);
     float mean = 0.f;
     if (!RMS) {
       float s[1] = {0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float h[8];
-        widen(now.h[c], h);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += h[e];
-      }
+      for (int c = 0; c < C; ++c) s[0] = sum8(now.h[c], s[0]);
       row_sum<WAVES, 1>(s, red0);
       mean = s[0] * inv;
     }
     float q[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float h[8];
-      opaque(now.h[c]);
-      widen(now.h[c], h);
+      float part = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = h[e] - mean;
-        q[0] += (c * TPR + tid) * 8 < p.K ? d * d : 0.f;
+        if (!RMS) h[c][e] -= mean;
+        part += h[c][e] * h[c][e];
       }
+      q[0] += (c * TPR + tid) * 8 < p.K ? part : 0.f;
     }
     row_sum<WAVES, 1>(q, red1);
     const float r = 1.0f / sqrtf(q[0] * inv + p.eps);
     float m[2] = {0.f, 0.f};
+    if (t < p.T) {  // a row behind the last is all zeros, whose r may be infinite
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * TPR + tid) * 8;
-      opaque(now.h[c]);
-      if (t >= p.T || col >= p.K) continue;
-      float h[8], g[8], w[8];
-      widen(now.h[c], h);
-      widen(now.g[c], g);
-      if (p.weight) ld8(p.weight + col, w);
+      for (int c = 0; c < C; ++c) {
+        widen(now.g[c], g[c]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = (h[e] - mean) * r;
-        dw[c][e] += g[e] * xh;
-        db[c][e] += g[e];
-        const float gw = p.weight ? g[e] * w[e] : g[e];
-        m[0] += gw;
-        m[1] += gw * xh;
+        for (int e = 0; e < 8; ++e) {
+          h[c][e] *= r;
+          dw[c][e] += g[c][e] * h[c][e];
+          db[c][e] += g[c][e];
+          g[c][e] *= w[c][e];
+          m[0] += g[c][e];
+          m[1] += g[c][e] * h[c][e];
+        }
       }
     }
     row_sum<WAVES, 2>(m, red2);
     const float m0 = RMS ? 0.f : m[0] * inv, m1 = m[1] * inv;
+    const RowBuffer rx(p.dx, p.lddx, t, p.K, t < p.T);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * TPR + tid) * 8;
-      opaque(now.h[c]);
-      opaque(now.g[c]);
-      if (t >= p.T || col >= p.K) continue;
-      float h[8], g[8], w[8], s[8];
-      widen(now.h[c], h);
-      widen(now.g[c], g);
-      widen(now.s[c], s);
-      if (p.weight) ld8(p.weight + col, w);
+      float s[8];
+      if (DSUM) widen(now.s[c], s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = (h[e] - mean) * r, gw = p.weight ? g[e] * w[e] : g[e];
-        g[e] = r * (gw - m0 - xh * m1) + s[e];
+        const float v = RMS ? g[c][e] - h[c][e] * m1 : g[c][e] - m0 - h[c][e] * m1;
+        g[c][e] = DSUM ? r * v + s[e] : r * v;
       }
-      *reinterpret_cast<uint4*>(p.dx + (long)t * p.lddx + col) = narrow(g);
+      rx.store((c * TPR + tid) * 8, narrow(g[c]));
+    }
+  };
+  const int stride = gridDim.x * ROWS;
+  Row ahead[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) ahead[i] = load((blockIdx.x + i * gridDim.x) * ROWS + group);
+  // whole rounds of AHEAD rows: those behind the last are buffers of no bytes
+  for (int t = blockIdx.x * ROWS + group; t < p.T + group; t += AHEAD * stride) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      Row now = ahead[i];
+      if (DSUM && !SUM_AHEAD) load_sum(t + i * stride, now);
+      ahead[i] = load(t + (i + AHEAD) * stride);
+      row(t + i * stride, now);
     }
   }
   // the workgroup's rows joined in LDS in order, into one row of partial sums
@@ -286,7 +300,7 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
 // Sums of the partial rows' columns, 64 columns a workgroup: 16 lanes of float4 by 64 rows, then a
 // fixed order.
 __global__ __launch_bounds__(1024) void k_norm_join(const float* __restrict__ part, int n_wg, int K, int n, float* first, float* second) {
-  __shared__ float4 red[64][16];
+  __shared__ float4 red[16][16];
   const int c4 = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const long all = (long)n * K, col = (long)blockIdx.x * 64 + 4 * c4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -297,11 +311,15 @@ __global__ __launch_bounds__(1024) void k_norm_join(const float* __restrict__ pa
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
   }
-  red[rg][c4] = v;
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) {
+    v.x += __shfl_xor(v.x, d); v.y += __shfl_xor(v.y, d); v.z += __shfl_xor(v.z, d); v.w += __shfl_xor(v.w, d);
+  }
+  if ((threadIdx.x & 63) < 16) red[threadIdx.x >> 6][c4] = v;
   __syncthreads();
   if (rg || col >= all) return;
-#pragma unroll 8
-  for (int w = 1; w < 64; ++w) {
+#pragma unroll
+  for (int w = 1; w < 16; ++w) {
     const float4 u = red[w][c4];
     v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
   }
@@ -312,18 +330,23 @@ __global__ __launch_bounds__(1024) void k_norm_join(const float* __restrict__ pa
 template <int TPR, int C, int WG>
 hipError_t launch_fwd(const NormParams& p, bool rms, hipStream_t s) {
   const dim3 grid((unsigned)((p.T + WG / TPR - 1) / (WG / TPR)));
-  if (rms) hipLaunchKernelGGL((k_norm<TPR, C, WG, true>), grid, dim3(WG), 0, s, p);
-  else hipLaunchKernelGGL((k_norm<TPR, C, WG, false>), grid, dim3(WG), 0, s, p);
+  if (rms && p.residual) hipLaunchKernelGGL((k_norm<TPR, C, WG, true, true>), grid, dim3(WG), 0, s, p);
+  else if (rms) hipLaunchKernelGGL((k_norm<TPR, C, WG, true, false>), grid, dim3(WG), 0, s, p);
+  else if (p.residual) hipLaunchKernelGGL((k_norm<TPR, C, WG, false, true>), grid, dim3(WG), 0, s, p);
+  else hipLaunchKernelGGL((k_norm<TPR, C, WG, false, false>), grid, dim3(WG), 0, s, p);
   return hipGetLastError();
 }
 
-template <int TPR, int C, int WG, bool AHEAD>
+template <int TPR, int C, int WG, int AHEAD>
 hipError_t launch_bwd(NormBwdParams p, bool rms, hipStream_t s) {
   constexpr int ROWS = WG / TPR;
   p.n_wg = std::min(NORM_BWD_WGS, (p.T + ROWS - 1) / ROWS);
   if (p.T > 0) {
-    if (rms) hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, true>), dim3(p.n_wg), dim3(WG), 0, s, p);
-    else hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, false>), dim3(p.n_wg), dim3(WG), 0, s, p);
+    const dim3 grid(p.n_wg), wg(WG);
+    if (rms && p.dsum) hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, true, true>), grid, wg, 0, s, p);
+    else if (rms) hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, true, false>), grid, wg, 0, s, p);
+    else if (p.dsum) hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, false, true>), grid, wg, 0, s, p);
+    else hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, false, false>), grid, wg, 0, s, p);
   }
   const int n = (p.dweight ? 1 : 0) + (p.dbias ? 1 : 0);
   if (n) {
@@ -336,18 +359,22 @@ hipError_t launch_bwd(NormBwdParams p, bool rms, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_norm(const NormParams& p, bool rms, hipStream_t s) {
+  if (p.K <= 512) return launch_fwd<64, 1, 64>(p, rms, s);
+  if (p.K <= 1024) return launch_fwd<128, 1, 128>(p, rms, s);
   if (p.K <= 2048) return launch_fwd<256, 1, 256>(p, rms, s);
   if (p.K <= 4096) return launch_fwd<256, 2, 256>(p, rms, s);
-  if (p.K <= 8192) return launch_fwd<256, 4, 256>(p, rms, s);
+  if (p.K <= 8192) return launch_fwd<512, 2, 512>(p, rms, s);
   return launch_fwd<1024, 2, 1024>(p, rms, s);
 }
 
 hipError_t launch_norm_bwd(const NormBwdParams& p, bool rms, hipStream_t s) {
-  if (p.K <= 512) return launch_bwd<64, 1, 1024, true>(p, rms, s);
-  if (p.K <= 2048) return launch_bwd<256, 1, 1024, true>(p, rms, s);
-  if (p.K <= 4096) return launch_bwd<256, 2, 512, true>(p, rms, s);
-  if (p.K <= 8192) return launch_bwd<512, 2, 512, true>(p, rms, s);
-  return launch_bwd<512, 4, 512, false>(p, rms, s);
+  if (p.K <= 512) return launch_bwd<64, 1, 512, 1>(p, rms, s);
+  if (p.K <= 1024) return launch_bwd<128, 1, 512, 1>(p, rms, s);
+  if (p.K <= 2048) return launch_bwd<128, 2, 512, 1>(p, rms, s);
+  if (p.K <= 4096) return launch_bwd<256, 2, 512, 1>(p, rms, s);
+  if (p.K <= 6144) return launch_bwd<384, 2, 768, 1>(p, rms, s);
+  if (p.K <= 8192) return launch_bwd<1024, 1, 1024, 1>(p, rms, s);
+  return launch_bwd<512, 4, 512, 1>(p, rms, s);
 }
 
 }  // namespace lora

@@ -43,7 +43,10 @@ struct NormBwdParams {
 };
 
 constexpr int NORM_MAX_K = 16384;
-constexpr int NORM_BWD_WGS = 256;  // most workgroups of the backward (one a CU) and rows of its partial sums
+#ifndef NBW
+#define NBW 256
+#endif
+constexpr int NORM_BWD_WGS = NBW;  // most workgroups of the backward (one a CU) and rows of its partial sums
 
 // An AdamW step over many tensors.
 struct AdamWParams {
