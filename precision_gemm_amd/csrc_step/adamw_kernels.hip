@@ -153,6 +153,7 @@ __device__ __forceinline__ void put(float* to, const Coef& c, bool on) {
 }
 // The same through the scalar cache (an earlier launch wrote them).
 typedef __attribute__((address_space(4))) const float c_float;
+__device__ __forceinline__ Coef get(const float* c) { return {c[0], c[1], c[2], c[3], c[4], c[5], c[6], c[7], c[8]}; }
 __device__ __forceinline__ Coef get(c_float* c) { return {c[0], c[1], c[2], c[3], c[4], c[5], c[6], c[7], c[8]}; }
 
 __device__ __forceinline__ double wave_sum(double s) {
@@ -443,29 +444,36 @@ __global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
   // lies in one row, and else to an odd length), B's by 8, which keeps its 16-byte pieces aligned.
   const bool pack_a = t.kind == KIND_A && (t.pack || t.pack_bwd), pack_b = t.kind == KIND_B && (t.pack || t.pack_bwd);
   const int ld = t.kind == KIND_A ? (t.cols % 4 == 0 ? t.cols + 4 : t.cols | 1) : 4 * at.len4 + 8;
+  __shared__ float shared_coef[ADAMW_COEF];
   int step = 0;
   auto coef = [&]() {
     if (!ALONE) return get(cp);
-    step = p.steps[t.group] + 1;
-    return coefficients(p.hyper + (long)t.group * ADAMW_HYPER, step, 1.0);
+    if (threadIdx.x < 64) {  // one wave for all: 64-bit arithmetic of all waves would take longer than the loads
+      step = p.steps[t.group] + 1;
+      const Coef c = coefficients(p.hyper + (long)t.group * ADAMW_HYPER, step, 1.0);
+      if (threadIdx.x == 0) put(shared_coef, c, true);
+    }
+    __syncthreads();
+    return get(shared_coef);
   };
   if (at.n & 3) update<BITS8, CLIP, PAST, WG, true>(t, at, s, ld, pack_a, pack_b, coef);
   else update<BITS8, CLIP, PAST, WG, false>(t, at, s, ld, pack_a, pack_b, coef);
-  if (ALONE || pack_a || pack_b) __syncthreads();
-  if (ALONE && threadIdx.x == 0) {
-    // every wave of this workgroup has read the group's step (its values depend on it)
+  if (ALONE && threadIdx.x == 0) {  // this workgroup has read the group's step
     if (add_agent(p.arrived + ADAMW_LINE * t.group, 1) == p.group_first[t.group + 1] - p.group_first[t.group] - 1) {
       p.steps[t.group] = step;
       set_agent(p.arrived + ADAMW_LINE * t.group, 0);
     }
   }
+  if (pack_a || pack_b) __syncthreads();
   if (pack_a) write_packs_a<WG>(s, ld, t.cols, tile.first, at.n / t.cols, t.rows, t.pack, t.cols % 8 ? t.pack_bwd : nullptr);
   if (pack_b) write_packs_b<WG>(s, ld, t.rows, tile.first, 4 * at.len4, t.cols, t.pack_bwd, t.pack);
 }
 
-// Steps of few tiles without norms are one launch.  More tiles than this and the arrivals at one
-// group's counter, one behind another, take longer than a launch for the groups.
-constexpr long ALONE_TILES = 256;
+// Steps of few tiles without norms are one launch.  Each arrival at a group's counter takes about 13 ns,
+// one behind another where all tiles are one group's, and goes on beside the other tiles' work: 80 tiles
+// 6.8 us with a launch for the groups, 6.1 without; 304 in 8 bits 13.0 and 12.0; 992 of one group 28.4
+// and 28.4; 816 of small tiles 18.3 and 18.7.
+constexpr long ALONE_TILES = 1024;
 
 // Steps of more tiles than this (8 million values, 250 MB and more) read and write their states and
 // master copies past the caches, which could not hold them until the next step: what the norms'

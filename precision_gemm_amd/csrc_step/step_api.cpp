@@ -4,7 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <new>
+#include <exception>
 #include <vector>
 
 #include "step_kernels.hpp"
@@ -105,7 +105,7 @@ lora_status lora_layer_norm(const uint16_t* x, int64_t ldx, const uint16_t* resi
   const lora_status st = check_norm(T, K, eps, rms);
   if (st != LORA_OK || T == 0) return st;
   if (!rows_ok(x, ldx, K) || !rows_ok(y, ldy, K) || !aligned(weight, 16) || !aligned(bias, 16) ||
-      (residual == nullptr) != (sum == nullptr) || (residual && (!rows_ok(residual, ldr, K) || !rows_ok(sum, lds, K))))
+      (residual == nullptr) != (sum == nullptr) || (sum && sum == y) || (residual && (!rows_ok(residual, ldr, K) || !rows_ok(sum, lds, K))))
     return LORA_ERR_INVALID_ARG;
   NormParams p{x, ldx, residual, ldr, T, K, weight, bias, eps, y, ldy, sum, lds};
   return launch_norm(p, rms, as_stream(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
@@ -167,7 +167,7 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
       for (int64_t at = 0; at < side; at += span) tiles[first[tensors[i].group]++] = {tensors[i], (int32_t)at, 0};
     }
     return LORA_OK;
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {  // no host memory for it
     return LORA_ERR_WORKSPACE;
   }
 }

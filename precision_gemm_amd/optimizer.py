@@ -3,7 +3,8 @@ the gradients that ``lora_backward`` leaves to the adapters in the forms that th
 backward read, in a few launches for all tensors.
 
 Each tensor belongs to a group, a tenant, with its own rates, step count and gradient norm.  Master
-copies are float32; states float32, or 8 bits with a scale for each 64 values.
+copies are float32; states float32, or 8 bits with a scale for each 64 values.  A step writes its
+buffers in place, without autograd's version counters.
 """
 
 from __future__ import annotations
@@ -72,7 +73,9 @@ def _check(t: torch.Tensor, name: str, dtype, numel: int, dev) -> int:
 class AdamW:
     """The tensors of a step with their states, cut into tiles once (lora_adamw_plan); the handle of
     :func:`adamw_step`.  ``steps`` int32 [n_groups] holds the steps that each group has made (zeros if
-    not given).  Calls on one handle must be ordered on one stream: they share its states and workspace."""
+    not given).  The handle holds the addresses of its tensors' buffers: gradients are written into
+    those (``lora_backward`` does), and adapters that are packed into new buffers need a new handle.
+    Calls on one handle must be ordered on one stream: they share its states and workspace."""
 
     def __init__(self, tensors: list, n_groups: int, *, state_bits: int = 32, steps: torch.Tensor | None = None):
         if state_bits not in (32, 8):

@@ -35,9 +35,9 @@ SIZES = [(dict(T=-1), INVALID), (dict(T=70000), UNSUPPORTED), (dict(K=0), INVALI
 @pytest.mark.parametrize("kw,status", SIZES + [
     (dict(x=NULL), INVALID), (dict(x=ODD), INVALID), (dict(ldx=56), INVALID), (dict(ldx=68), INVALID), (dict(res=ODD), INVALID),
     (dict(res=NULL), INVALID), (dict(sum=NULL), INVALID), (dict(ldr=56), INVALID), (dict(lds=60), INVALID), (dict(y=NULL), INVALID),
-    (dict(ldy=63), INVALID), (dict(w=ODD), INVALID), (dict(b=ODD), INVALID), (dict(T=0, x=NULL), OK)])
+    (dict(ldy=63), INVALID), (dict(sum=ctypes.c_void_p(0x2000)), INVALID), (dict(w=ODD), INVALID), (dict(b=ODD), INVALID), (dict(T=0, x=NULL), OK)])
 def test_layer_norm(L, kw, status):
-    base = dict(x=FAKE, ldx=64, res=FAKE, ldr=64, T=3, K=64, w=FAKE, b=FAKE, eps=1e-6, rms=0, y=FAKE, ldy=64, sum=FAKE, lds=64,
+    base = dict(x=FAKE, ldx=64, res=FAKE, ldr=64, T=3, K=64, w=FAKE, b=FAKE, eps=1e-6, rms=0, y=ctypes.c_void_p(0x2000), ldy=64, sum=FAKE, lds=64,
                 stream=NULL)
     assert call(L.lora_layer_norm, "x ldx res ldr T K w b eps rms y ldy sum lds stream", base, **kw) == status
 
