@@ -82,38 +82,45 @@ __device__ __forceinline__ bool load_positions(const int* positions, int T, int 
 }
 
 // Rows of the table for this lane by its pairs' axes.  A quad of pairs on one axis is still one
-// 16-byte load of cosines and one of sines; otherwise every value is loaded by itself.
+// 16-byte load of cosines and one of sines.  Otherwise the wave puts the token's row together in `row`
+// (256 floats of LDS, its own): a lane loads a pair's cosine and sine (two, with heads of 256), and takes
+// its eight pairs from there.  4,096 tokens of 32 + 8 + 8 heads of 128: forward by quads 17.1 us, by
+// pairs 17.3 (each lane loading its sixteen values by itself 30.3); into an 8-bit cache 20.3 and 21.2 (35.6).
 template <int AXES>
 __device__ __forceinline__ Turn load_turn(const float* cos_sin, const int (&pos)[4], int rot, const LaneMap& m,
-                                          const AxisMap& axes) {
+                                          const AxisMap& axes, float* row) {
   if (AXES == ONE_AXIS) return load_turn(cos_sin, pos[0], rot, m);
+  const int half = rot >> 1, p0 = pos[0], p1 = pos[1], p2 = pos[2], p3 = pos[3];
+  auto table = [=](int axis) {
+    const int lo = axis & 1 ? p1 : p0, hi = axis & 1 ? p3 : p2;
+    return cos_sin + (long)(axis & 2 ? hi : lo) * rot;
+  };
+  if (AXES == AXIS_PAIRS) {
+    const int lane = threadIdx.x & 63;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // behind the reads of the last token's row
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 64 * k + lane;
+      if (i < half) {
+        const uint64_t w = lane < 32 ? axes.pair[2 * k] : axes.pair[2 * k + 1];
+        const float* r = table((int)(w >> (2 * (i & 31))) & 3) + i;
+        row[i] = r[0];
+        row[half + i] = r[half];
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
   Turn t;
 #pragma unroll
   for (int e = 0; e < 8; ++e) { t.c[e] = 1.f; t.s[e] = 0.f; }
   if (!m.turns) return t;
-  const int half = rot >> 1, p0 = pos[0], p1 = pos[1], p2 = pos[2], p3 = pos[3];
-  auto row = [=](int axis) {
-    const int lo = axis & 1 ? p1 : p0, hi = axis & 1 ? p3 : p2;
-    return cos_sin + (long)(axis & 2 ? hi : lo) * rot;
-  };
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int at = q ? m.t1 : m.t0;
-    if (AXES == AXIS_QUADS) {
-      const float* r = row((int)(axes.quad >> (at >> 1)) & 3) + at;
-      const float4 c = *reinterpret_cast<const float4*>(r), s = *reinterpret_cast<const float4*>(r + half);
-      t.c[4 * q] = c.x; t.c[4 * q + 1] = c.y; t.c[4 * q + 2] = c.z; t.c[4 * q + 3] = c.w;
-      t.s[4 * q] = s.x; t.s[4 * q + 1] = s.y; t.s[4 * q + 2] = s.z; t.s[4 * q + 3] = s.w;
-    } else {
-      const uint64_t w = at < 64 ? (at < 32 ? axes.pair[0] : axes.pair[1]) : (at < 96 ? axes.pair[2] : axes.pair[3]);
-      const int four = (int)(w >> (2 * (at & 31)));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float* r = row(four >> (2 * e)) + at + e;
-        t.c[4 * q + e] = r[0];
-        t.s[4 * q + e] = r[half];
-      }
-    }
+    const float* r = AXES == AXIS_PAIRS ? row + at : table((int)(axes.quad >> (at >> 1)) & 3) + at;
+    const float4 c = *reinterpret_cast<const float4*>(r), s = *reinterpret_cast<const float4*>(r + half);
+    t.c[4 * q] = c.x; t.c[4 * q + 1] = c.y; t.c[4 * q + 2] = c.z; t.c[4 * q + 3] = c.w;
+    t.s[4 * q] = s.x; t.s[4 * q + 1] = s.y; t.s[4 * q + 2] = s.z; t.s[4 * q + 3] = s.w;
   }
   return t;
 }
@@ -147,11 +154,17 @@ __device__ __forceinline__ uint4 narrow(const float* v) {
   return make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
 }
 
-// Sum over the LPH neighbouring lanes of a head.
+// Sum over the LPH neighbouring lanes of a head (4, 8 or 16: within a row of lanes, so on the DPP path).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < LPH; d <<= 1) v += __shfl_xor(v, d);
+  v = dpp_add<0xb1>(v);                  // its neighbour
+  v = dpp_add<0x4e>(v);                  // the other pair of four
+  if (LPH > 4) v = dpp_add<0x141>(v);    // the other four of eight
+  if (LPH > 8) v = dpp_add<0x140>(v);    // the other eight
   return v;
 }
 
@@ -203,7 +216,8 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
     }
     if (!placed) slot = -1;
   }
-  const Turn tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes);
+  __shared__ __attribute__((aligned(16))) float rows[AXES == AXIS_PAIRS ? 4 : 1][AXES == AXIS_PAIRS ? 256 : 4];
+  const Turn tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes, rows[AXES == AXIS_PAIRS ? threadIdx.x >> 6 : 0]);
 
   float v[16];
   widen(xa, v);
@@ -258,6 +272,7 @@ template <int D, int AXES>
 __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH, ROWS = 4 * SLOTS;
   __shared__ __attribute__((aligned(16))) float red[ROWS][D];
+  __shared__ __attribute__((aligned(16))) float rows[AXES == AXIS_PAIRS ? 4 : 1][AXES == AXIS_PAIRS ? 256 : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int sl = lane / LPH, j = lane % LPH;
   const LaneMap m = lane_map(j, p.rot, p.interleaved);
@@ -284,9 +299,18 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
     return Round{g.load(at + m.a), g.load(at + m.b), x.load(at + m.a), x.load(at + m.b)};
   };
 
-  float acc[16];
+  // the weights stay in registers: loaded in each round, they would be waited for behind the next
+  // round's loads, which come before them
+  float acc[16], ww[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int e = 0; e < 16; ++e) acc[e] = ww[e] = 0.f;
+  if (w) {
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4) {
+      const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
+      ww[4 * q4] = w4.x; ww[4 * q4 + 1] = w4.y; ww[4 * q4 + 2] = w4.z; ww[4 * q4 + 3] = w4.w;
+    }
+  }
   int t = first / rounds, r = first - t * rounds;
   Round next = load(t, r, first < last);
   bool placed = true, fresh = true;
@@ -298,7 +322,7 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
       int pos[4] = {0, 0, 0, 0};
       placed = p.rot == 0 || load_positions<AXES>(p.positions, p.T, t0, p.max_pos, p.axes, pos);
       if (!placed && p.status && lane == 0) or_agent(p.status, ST_POSITION);
-      tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes);
+      tn = load_turn<AXES>(p.cos_sin, pos, p.rot, m, p.axes, rows[AXES == AXIS_PAIRS ? wave : 0]);
     }
     fresh = ++r == rounds;
     if (fresh) {
@@ -332,17 +356,11 @@ __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
       float dot = 0.f;
       const bool count = live && placed;
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        const float4 w4 = *reinterpret_cast<const float4*>(w + (q4 < 2 ? m.a : m.b - 8) + 4 * q4);
-        const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 4 * q4 + i;
-          x[e] *= rs;                       // xh
-          acc[e] += count ? g[e] * x[e] : 0.f;
-          g[e] *= ww[i];
-          dot += g[e] * x[e];
-        }
+      for (int e = 0; e < 16; ++e) {
+        x[e] *= rs;                       // xh
+        acc[e] += count ? g[e] * x[e] : 0.f;
+        g[e] *= ww[e];
+        dot += g[e] * x[e];
       }
       const float mean = head_sum<LPH>(dot) * (1.0f / D);
 #pragma unroll

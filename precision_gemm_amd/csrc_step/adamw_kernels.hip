@@ -11,6 +11,13 @@
 // States in 8 bits: blocks of 64 values share a scale (the largest magnitude / 448); a value is an
 // e4m3 code.  Of v its root is held, which halves the exponents that a code has to span; a root that
 // is not 0 keeps a code that is not (0 would make the next step as large as m / eps).
+//
+// Bound by HBM: 59 instructions a value with states in 32 bits, 94 in 8, beside 28 and 16 bytes of
+// states and master copies and 6 of bf16 forms.  A workgroup takes a tile whose bf16 form it has in LDS,
+// so that the packed forms, one of which is always across the tensor's rows, leave in whole 16-byte
+// pieces in the same pass (repacking by launches of their own would be two for each adapter).  32 tenants of rank 16
+// on four projections (35.7 million values, 1.21 GB; 0.79 in 8 bits): 195 us, 6.2 TB/s, and 146, 5.4; a
+// copy of as many bytes reaches 5.1.
 #include <algorithm>
 
 #include "step_kernels.hpp"
@@ -162,9 +169,38 @@ __device__ __forceinline__ double wave_sum(double s) {
   return s;
 }
 
-// Sums of the squares of the tiles' gradients, a wave a tile, all its loads in flight at once.
+// Settles a group from the sum of its gradients' squares: norm, step, coefficients.  One thread.
+__device__ __forceinline__ void settle(const AdamWParams& p, int g, bool on, double sum) {
+  const double* h = p.hyper + (long)g * ADAMW_HYPER;
+  double clip = 1.0;
+  if (p.norm) {
+    const double norm = sqrt(sum);
+    p.norm[g] = (float)norm;
+    if (h[5] > 0.0) clip = fmin(1.0, h[5] / (norm + 1e-6));
+    if (!(norm <= 1.7976931348623157e308)) {
+      on = false;
+      if (p.status) or_agent(p.status, LORA_ADAMW_NOT_FINITE);
+    }
+  }
+  const int step = p.steps[g] + 1;
+  if (on) p.steps[g] = step;
+  put(p.coef + (long)g * ADAMW_COEF, coefficients(h, step, clip), on);
+}
+
+// Sums of the squares of the tiles' gradients, a wave a tile, all its loads in flight at once.  35.7
+// million gradients (143 MB) behind an update: 39 us, 3.7 TB/s, with that update's stores still on
+// their way to memory (alone 31 us, 4.6); two or four waves a tile do not change it.
+// LAST: the wave that is the last of its group settles the group (its sums in their order, whichever
+// wave that is), and workgroups behind the tiles' settle the groups that make no step.
+template <bool LAST>
 __global__ __launch_bounds__(256) void k_adamw_norms(AdamWParams p) {
   const int lane = threadIdx.x & 63;
+  const long n_wg = (p.n_tiles + 3) / 4;
+  if (LAST && blockIdx.x >= n_wg) {
+    const int g = (int)(blockIdx.x - n_wg) * 256 + threadIdx.x;
+    if (g < p.n_groups && ((p.active && !p.active[g]) || p.group_first[g] == p.group_first[g + 1])) settle(p, g, false, 0.0);
+    return;
+  }
   const long at = (long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (at >= p.n_tiles) return;
   const lora_adamw_tile tile = p.tiles[at];
@@ -192,17 +228,33 @@ __global__ __launch_bounds__(256) void k_adamw_norms(AdamWParams p) {
     s += (double)e.x * e.x + (double)e.y * e.y + (double)e.z * e.z;
   }
   s = wave_sum(s);
-  if (lane == 0) p.part[at] = s;
+  if (!LAST) {
+    if (lane == 0) p.part[at] = s;
+    return;
+  }
+  const int first = p.group_first[t.group], last = p.group_first[t.group + 1];
+  int before = 0;
+  if (lane == 0) {
+    st_agent_u64(reinterpret_cast<uint64_t*>(p.part + at), __builtin_bit_cast(uint64_t, s));
+    wait_stores();
+    before = add_agent(p.arrived + ADAMW_LINE * t.group, 1);
+  }
+  if (__builtin_amdgcn_readfirstlane(before) != last - first - 1) return;
+  s = 0.0;
+  for (int i = first + lane; i < last; i += 64)
+    s += __builtin_bit_cast(double, ld_agent_u64(reinterpret_cast<const uint64_t*>(p.part + i)));
+  s = wave_sum(s);
+  if (lane) return;
+  set_agent(p.arrived + ADAMW_LINE * t.group, 0);
+  settle(p, t.group, true, s);
 }
 
-// A group's norm (its tiles' sums in a fixed order), step and coefficients.
+// The groups, a workgroup each, where the norms' launch does not settle them (or there is none).
 __global__ __launch_bounds__(256) void k_adamw_groups(AdamWParams p) {
   __shared__ double red[4];
   const int g = blockIdx.x, first = p.group_first[g], last = p.group_first[g + 1];
-  bool on = (!p.active || p.active[g]) && first != last;
-  double clip = 1.0, s = 0.0;
-  const double* h = p.hyper + (long)g * ADAMW_HYPER;
-  const int step = p.steps[g] + 1;
+  const bool on = (!p.active || p.active[g]) && first != last;
+  double s = 0.0;
   if (p.norm && on) {
 #pragma unroll 8
     for (int i = first + threadIdx.x; i < last; i += 256) s += p.part[i];
@@ -210,18 +262,7 @@ __global__ __launch_bounds__(256) void k_adamw_groups(AdamWParams p) {
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x) return;
-  if (p.norm) {
-    const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
-    p.norm[g] = (float)norm;
-    if (h[5] > 0.0) clip = fmin(1.0, h[5] / (norm + 1e-6));
-    if (!(norm <= 1.7976931348623157e308)) {
-      on = false;
-      if (p.status) or_agent(p.status, LORA_ADAMW_NOT_FINITE);
-    }
-  }
-  if (on) p.steps[g] = step;
-  put(p.coef + (long)g * ADAMW_COEF, coefficients(h, step, clip), on);
+  if (threadIdx.x == 0) settle(p, g, on, (red[0] + red[1]) + (red[2] + red[3]));
 }
 
 // e4m3 codes, to nearest even.  No clamp: a value is at most its block's largest times 448 / largest, a
@@ -426,7 +467,9 @@ __device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& 
   }
 }
 
-// A workgroup a tile.  ALONE: the launch is the whole step (no norms, few tiles): every workgroup works
+// A workgroup a tile, a quad a thread: 1,024 threads (256 with four quads each, and 512 with two, took 3 %
+// and 1.5 % longer on the layer above, 6.4 and 5.8 us against 5.4 on one adapter of rank 8: more code to
+// fetch for fewer waves).  ALONE: the launch is the whole step (no norms, few tiles): every workgroup works
 // out its group's coefficients while its loads are in flight, and the group's last counts its step.
 template <bool BITS8, bool CLIP, bool ALONE, bool PAST, int WG>
 __global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
@@ -475,9 +518,15 @@ __global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
 // and 28.4; 816 of small tiles 18.3 and 18.7.
 constexpr long ALONE_TILES = 1024;
 
+// With norms, the groups of so few tiles are settled in the norms' launch by the same arrivals (32 tiles
+// 11.7 us with a launch for the groups, 9.6 without; 80 12.0 and 10.9; 304 of one group 17.0 and 19.5).
+constexpr long LAST_TILES = 128;
+
 // Steps of more tiles than this (8 million values, 250 MB and more) read and write their states and
 // master copies past the caches, which could not hold them until the next step: what the norms'
-// launch has read of the gradients then stays for the update.
+// launch has read of the gradients then stays for the update (the layer above: 265 us within them, 237
+// past them, with norms).  Codes and scales of 8-bit states stay within: a wave's 256 bytes are too
+// short for it (188 us with all within the caches, 180 with the master copies past them, 190 with all).
 constexpr long STREAM_TILES = 2048;
 
 constexpr int WG = 1024;
@@ -496,9 +545,11 @@ void launch_update(const AdamWParams& p, bool alone, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_adamw(const AdamWParams& p, int state_bits, hipStream_t s) {
-  const bool alone = !p.norm && p.n_tiles <= ALONE_TILES;
-  if (p.norm && p.n_tiles) hipLaunchKernelGGL(k_adamw_norms, dim3((unsigned)((p.n_tiles + 3) / 4)), dim3(256), 0, s, p);
-  if (!alone) hipLaunchKernelGGL(k_adamw_groups, dim3(p.n_groups), dim3(256), 0, s, p);
+  const bool alone = !p.norm && p.n_tiles <= ALONE_TILES, last = p.norm && p.n_tiles <= LAST_TILES;
+  const unsigned norm_wgs = (unsigned)((p.n_tiles + 3) / 4);
+  if (last) hipLaunchKernelGGL(k_adamw_norms<true>, dim3(norm_wgs + (p.n_groups + 255) / 256), dim3(256), 0, s, p);
+  else if (p.norm) hipLaunchKernelGGL(k_adamw_norms<false>, dim3(norm_wgs), dim3(256), 0, s, p);
+  if (!alone && !last) hipLaunchKernelGGL(k_adamw_groups, dim3(p.n_groups), dim3(256), 0, s, p);
   if (p.n_tiles == 0) return hipGetLastError();
   if (state_bits == 8) launch_update<true>(p, alone, s);
   else launch_update<false>(p, alone, s);

@@ -6,6 +6,9 @@
 // and backwards, with g = dy w:
 //   dh = r (g - mean(g) - xh mean(g xh))   (without mean(g) for the RMS norm)
 //   dw = sum over the rows of dy xh,  db = sum of dy.
+//
+// Bound by HBM; a row is read once and held in registers, so the squares are summed about the mean (and
+// the backward takes the statistics anew, without reading anything for it).
 #include <algorithm>
 
 #include "step_kernels.hpp"
@@ -76,7 +79,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*slot)[N]) {
   }
 }
 
-// TPR threads a row, C chunks of 8 values a thread, WG threads a workgroup.
+// TPR threads a row, C chunks of 8 values a thread, WG threads a workgroup.  4,096 rows of 4,096 values
+// with a residual (134 MB): 21.0 us, 6.4 TB/s (a copy of as many bytes 26).  Loads under a condition
+// instead of bounded buffers: 25.
 template <int TPR, int C, int WG, bool RMS, bool RES>
 __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
   constexpr int WAVES = TPR / 64;
@@ -149,7 +154,11 @@ __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
 
 // Backward.  A workgroup takes rows blockIdx.x * (WG / TPR) + ... in strides of the grid, the loads of
 // the next AHEAD of them in flight; a thread meets the same columns in every row, so it keeps their
-// weights, and their sums for the weights' gradients, in registers.
+// weights, and their sums for the weights' gradients, in registers.  One workgroup a CU (256 in all), for
+// each leaves a row of partial sums (512: 20 % longer).  Sums meet a wave's lanes by DPP and its
+// workgroup's waves through LDS, three times a row; what would overlap badly across the barriers is few
+// instructions (24 a value).  4,096 rows of 4,096 values, with the residual stream's gradient (134 MB): 25.9 us, 5.2
+// TB/s, and k_norm_join.  Loads under a condition (which wait for the next row's): 36.
 template <int TPR, int C, int WG, int AHEAD, bool RMS, bool DSUM>
 __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
   constexpr int WAVES = TPR / 64, ROWS = WG / TPR;
@@ -258,10 +267,11 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
       row(t + i * stride, now);
     }
   }
-  // the workgroup's rows joined in LDS in order, into one row of partial sums
+  // the workgroup's rows joined in LDS in order, into one row of partial sums, or the result
   const int n = (p.dweight ? 1 : 0) + (p.dbias ? 1 : 0);
-  float* out = p.part + (long)blockIdx.x * n * p.K;
-  auto write = [&](float (&a)[C][8]) {
+  float* row_out = p.part + (long)blockIdx.x * n * p.K;
+  auto write = [&](float (&a)[C][8], float* result) {
+    float* out = p.n_wg == 1 ? result : row_out;
     if (ROWS > 1) {
       __syncthreads();
       if (group > 0) {
@@ -291,14 +301,14 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
         }
       }
     }
-    out += p.K;
+    row_out += p.K;
   };
-  if (p.dweight) write(dw);
-  if (p.dbias) write(db);
+  if (p.dweight) write(dw, p.dweight);
+  if (p.dbias) write(db, p.dbias);
 }
 
 // Sums of the partial rows' columns, 64 columns a workgroup: 16 lanes of float4 by 64 rows, then a
-// fixed order.
+// fixed order.  256 rows of 8,192 (8.4 MB): 4.8 us, a launch and four rounds of loads.
 __global__ __launch_bounds__(1024) void k_norm_join(const float* __restrict__ part, int n_wg, int K, int n, float* first, float* second) {
   __shared__ float4 red[16][16];
   const int c4 = threadIdx.x & 15, rg = threadIdx.x >> 4;
@@ -349,7 +359,7 @@ hipError_t launch_bwd(NormBwdParams p, bool rms, hipStream_t s) {
     else hipLaunchKernelGGL((k_norm_bwd<TPR, C, WG, AHEAD, false, false>), grid, wg, 0, s, p);
   }
   const int n = (p.dweight ? 1 : 0) + (p.dbias ? 1 : 0);
-  if (n) {
+  if (n && p.n_wg != 1) {  // one workgroup's sums are the result
     float *a = p.dweight ? p.dweight : p.dbias, *b = p.dbias;
     hipLaunchKernelGGL(k_norm_join, dim3((unsigned)(((long)n * p.K + 63) / 64)), dim3(1024), 0, s, p.part, p.n_wg, p.K, n, a, b);
   }
@@ -358,6 +368,10 @@ hipError_t launch_bwd(NormBwdParams p, bool rms, hipStream_t s) {
 
 }  // namespace
 
+// Threads and chunks by the row's width.  8,192 rows of 512: one wave a row 7.3 us, a workgroup of 256
+// threads 12.6; 4,096 rows of 4,096 (256 threads, 2 chunks 21.2 us; 512 x 1 21.4, 128 x 4 22.0, 64 x 8 23.6)
+// and of 8,192 (512 x 2 42.5; 256 x 4 43.5, 1024 x 1 44.3, 128 x 8 46.0); 2,048 of 16,384 (1024 x 2 47.6;
+// 512 x 4 49.6, 256 x 8 50.0).
 hipError_t launch_norm(const NormParams& p, bool rms, hipStream_t s) {
   if (p.K <= 512) return launch_fwd<64, 1, 64>(p, rms, s);
   if (p.K <= 1024) return launch_fwd<128, 1, 128>(p, rms, s);
@@ -367,6 +381,11 @@ hipError_t launch_norm(const NormParams& p, bool rms, hipStream_t s) {
   return launch_fwd<1024, 2, 1024>(p, rms, s);
 }
 
+// The same, and rows at a time of a workgroup (its threads by those of a row).  With k_norm_join: 8,192 rows
+// of 512 in workgroups of 512 threads 11.3 us, of 1,024 11.8, of 256 12.4; of 2,048 (128 threads, 2 chunks,
+// 4 rows 23.2; 256 x 1, 4 rows 24.0); 4,096 of 4,096 (256 x 2, 2 rows 30.2, two rows ahead 30.2; 512 x 1,
+// 2 rows 31.1); 1,001 of 5,376 (384 x 2, 2 rows 13.1; 512 x 2 15.6); 4,096 of 8,192 (1024 x 1 49.7; 512 x 2
+// 50.9); 2,048 of 16,384 (512 x 4 66; 1024 x 2 spills, 89).
 hipError_t launch_norm_bwd(const NormBwdParams& p, bool rms, hipStream_t s) {
   if (p.K <= 512) return launch_bwd<64, 1, 512, 1>(p, rms, s);
   if (p.K <= 1024) return launch_bwd<128, 1, 512, 1>(p, rms, s);

@@ -43,10 +43,7 @@ struct NormBwdParams {
 };
 
 constexpr int NORM_MAX_K = 16384;
-#ifndef NBW
-#define NBW 256
-#endif
-constexpr int NORM_BWD_WGS = NBW;  // most workgroups of the backward (one a CU) and rows of its partial sums
+constexpr int NORM_BWD_WGS = 256;  // most workgroups of the backward (one a CU) and rows of its partial sums
 
 // An AdamW step over many tensors.
 struct AdamWParams {
