@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -65,10 +67,8 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build the HIP library)")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES],
-           *[os.path.join(CSRC_ATTN, s) for s in SOURCES_ATTN], *[os.path.join(CSRC_STEP, s) for s in SOURCES_STEP]]
+def _run(cmd: list, verbose: bool) -> str:
+    """Run a compiler; its remarks (stderr), with anything else printed or raised."""
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -79,9 +79,22 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{errs}")
     if verbose and errs.strip():
         print(errs, file=sys.stderr)
+    return res.stderr
+
+
+def build(verbose: bool = False) -> str:
+    tmp = LIB + ".tmp"
+    sources = [os.path.join(d, s) for d, names in ((CSRC, SOURCES), (CSRC_ATTN, SOURCES_ATTN), (CSRC_STEP, SOURCES_STEP))
+               for s in names]
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+    # a compiler a source, side by side: one after another they take three minutes
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(objects, f"{i}.o") for i in range(len(sources))]
+        remarks = list(pool.map(lambda so: _run([hipcc(), *compile_flags, "-c", so[0], "-o", so[1]], verbose), zip(sources, objs)))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
     with open(RESOURCES, "w") as f:
-        json.dump(parse_resources(res.stderr), f, indent=1, sort_keys=True)
+        json.dump(parse_resources("\n".join(remarks)), f, indent=1, sort_keys=True)
     for binding, source in BINDINGS.items():
         build_binding(binding, source, verbose)
     return LIB

@@ -266,8 +266,8 @@ __global__ __launch_bounds__(256) void k_norm_rope(RopeParams p) {
 // pairs of its kind, the next round's loads in flight while one is computed.  The sums are
 // joined over the wave's slots and the workgroup's waves in LDS, in a fixed order, into one row
 // a workgroup, which k_weight_grad adds in order (no atomics: the result does not depend on
-// timing).  4,096 tokens of 32 + 8 + 8 heads of 128 (145 MB): 31.9 us, 4.5 TB/s; 512 workgroups
-// instead of 768 take 8 % longer, 256 55 %; two rounds in flight instead of one 3 %.
+// timing).  4,096 tokens of 32 + 8 + 8 heads of 128 (145 MB): 29.4 us, 4.9 TB/s (31.9 with loads under
+// conditions and weights loaded in each round); 512 workgroups instead of 768 take 8 % longer, 256 55 %.
 template <int D, int AXES>
 __global__ __launch_bounds__(256, 3) void k_norm_rope_bwd(RopeBwdParams p) {
   constexpr int LPH = D / 16, SLOTS = 64 / LPH, ROWS = 4 * SLOTS;

@@ -16,7 +16,7 @@
 // states and master copies and 6 of bf16 forms.  A workgroup takes a tile whose bf16 form it has in LDS,
 // so that the packed forms, one of which is always across the tensor's rows, leave in whole 16-byte
 // pieces in the same pass (repacking by launches of their own would be two for each adapter).  32 tenants of rank 16
-// on four projections (35.7 million values, 1.21 GB; 0.79 in 8 bits): 195 us, 6.2 TB/s, and 146, 5.4; a
+// on four projections (35.7 million values, 1.21 GB; 0.79 in 8 bits): 195 us, 6.2 TB/s, and 152, 5.2; a
 // copy of as many bytes reaches 5.1.
 #include <algorithm>
 
@@ -188,7 +188,7 @@ __device__ __forceinline__ void settle(const AdamWParams& p, int g, bool on, dou
 }
 
 // Sums of the squares of the tiles' gradients, a wave a tile, all its loads in flight at once.  35.7
-// million gradients (143 MB) behind an update: 39 us, 3.7 TB/s, with that update's stores still on
+// million gradients (143 MB) behind an update: 38 us, 3.8 TB/s, with that update's stores still on
 // their way to memory (alone 31 us, 4.6); two or four waves a tile do not change it.
 // LAST: the wave that is the last of its group settles the group (its sums in their order, whichever
 // wave that is), and workgroups behind the tiles' settle the groups that make no step.

@@ -80,7 +80,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*slot)[N]) {
 }
 
 // TPR threads a row, C chunks of 8 values a thread, WG threads a workgroup.  4,096 rows of 4,096 values
-// with a residual (134 MB): 21.0 us, 6.4 TB/s (a copy of as many bytes 26).  Loads under a condition
+// with a residual (134 MB): 21.5 us, 6.2 TB/s (a copy of as many bytes 26).  Loads under a condition
 // instead of bounded buffers: 25.
 template <int TPR, int C, int WG, bool RMS, bool RES>
 __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
 // weights, and their sums for the weights' gradients, in registers.  One workgroup a CU (256 in all), for
 // each leaves a row of partial sums (512: 20 % longer).  Sums meet a wave's lanes by DPP and its
 // workgroup's waves through LDS, three times a row; what would overlap badly across the barriers is few
-// instructions (24 a value).  4,096 rows of 4,096 values, with the residual stream's gradient (134 MB): 25.9 us, 5.2
+// instructions (24 a value).  4,096 rows of 4,096 values, with the residual stream's gradient (134 MB): 26.6 us, 5.0
 // TB/s, and k_norm_join.  Loads under a condition (which wait for the next row's): 36.
 template <int TPR, int C, int WG, int AHEAD, bool RMS, bool DSUM>
 __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
 }
 
 // Sums of the partial rows' columns, 64 columns a workgroup: 16 lanes of float4 by 64 rows, then a
-// fixed order.  256 rows of 8,192 (8.4 MB): 4.8 us, a launch and four rounds of loads.
+// fixed order.  256 rows of 8,192 (8.4 MB): 4.6 us, a launch and four rounds of loads.
 __global__ __launch_bounds__(1024) void k_norm_join(const float* __restrict__ part, int n_wg, int K, int n, float* first, float* second) {
   __shared__ float4 red[16][16];
   const int c4 = threadIdx.x & 15, rg = threadIdx.x >> 4;
