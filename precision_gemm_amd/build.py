@@ -87,7 +87,7 @@ def build(verbose: bool = False) -> str:
     sources = [os.path.join(d, s) for d, names in ((CSRC, SOURCES), (CSRC_ATTN, SOURCES_ATTN), (CSRC_STEP, SOURCES_STEP))
                for s in names]
     compile_flags = [f for f in FLAGS if f != "-shared"]
-    # a compiler a source, side by side: one after another they take three minutes
+    # a compiler a source, side by side: lora_kernels.hip takes as long as all others do one after another
     with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
         objs = [os.path.join(objects, f"{i}.o") for i in range(len(sources))]
         remarks = list(pool.map(lambda so: _run([hipcc(), *compile_flags, "-c", so[0], "-o", so[1]], verbose), zip(sources, objs)))
@@ -95,8 +95,8 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     with open(RESOURCES, "w") as f:
         json.dump(parse_resources("\n".join(remarks)), f, indent=1, sort_keys=True)
-    for binding, source in BINDINGS.items():
-        build_binding(binding, source, verbose)
+    with ThreadPoolExecutor(len(BINDINGS)) as pool:
+        list(pool.map(lambda b: build_binding(*b, verbose), BINDINGS.items()))
     return LIB
 
 
