@@ -358,7 +358,7 @@ __device__ __forceinline__ void write_packs_b(const uint16_t* s, int ld, int r, 
 }
 
 // The update of a tile in the registers of WG threads, and its bf16 form into LDS.  PART: the tile is the
-// end of a vector of no whole number of quads.
+// end of a vector of no whole number of blocks; lanes behind the end are nothing to the last block's scale.
 template <bool BITS8, bool CLIP, bool PAST, int WG, bool PART, typename GetCoef>
 __device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& at, uint16_t* s, int ld, bool pack_a, bool pack_b,
                                        GetCoef&& get_coef) {
@@ -499,7 +499,7 @@ __global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
     __syncthreads();
     return get(shared_coef);
   };
-  if (at.n & 3) update<BITS8, CLIP, PAST, WG, true>(t, at, s, ld, pack_a, pack_b, coef);
+  if (at.n % ADAMW_BLOCK) update<BITS8, CLIP, PAST, WG, true>(t, at, s, ld, pack_a, pack_b, coef);
   else update<BITS8, CLIP, PAST, WG, false>(t, at, s, ld, pack_a, pack_b, coef);
   if (ALONE && threadIdx.x == 0) {  // this workgroup has read the group's step
     if (add_agent(p.arrived + ADAMW_LINE * t.group, 1) == p.group_first[t.group + 1] - p.group_first[t.group] - 1) {

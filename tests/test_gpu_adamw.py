@@ -196,6 +196,7 @@ class Case:
 SHAPES = {
     "one value": [("plain", 1, 1, 0)],
     "short vectors": [("plain", 1, n, n % 2) for n in (1, 2, 3, 5, 63, 64, 65, 127, 4095, 4096, 4097, 8191)],
+    "vectors of whole quads": [("plain", 1, n, n % 3) for n in (4, 8, 60, 100, 196, 396, 1000, 4100, 8188)],
     "rank 1": [("A", 4160, 1, 0), ("B", 1, 4160, 0), ("A", 64, 1, 0), ("B", 1, 64, 1)],
     "rank 2 and 3": [("A", 2112, 2, 0), ("B", 2, 2112, 0), ("A", 1344, 3, 1), ("B", 3, 1408, 1)],
     "rank 8": [("A", 4096, 8, 0), ("B", 8, 6144, 0)],
