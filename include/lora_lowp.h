@@ -625,7 +625,7 @@ typedef struct lora_adamw_tile {
  * group_first into device memory for lora_adamw_step.  LORA_ERR_INVALID_ARG also where a buffer that a
  * step writes overlaps another of its buffers (a tensor given twice); LORA_ERR_WORKSPACE where the host
  * has no memory for the check.
- * Limits: n <= 2^20, n_groups <= 8192, fewer than 2^31 tiles. */
+ * Limits: n <= 2^20, n_groups <= 8192, fewer than 2^22 tiles (17 billion values in tiles of 4,096). */
 lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t n_groups, int32_t state_bits,
                             int64_t* n_tiles, lora_adamw_tile* tiles, int32_t* group_first);
 

@@ -16,7 +16,7 @@ namespace {
 constexpr int MAX_TOKENS = 65536;
 constexpr int MAX_GROUPS = 8192;
 constexpr int MAX_TENSORS = 1 << 20;
-constexpr int64_t MAX_TILES = INT32_MAX;
+constexpr int64_t MAX_TILES = (1 << 22) - 1;  // of 1,024 threads: a launch has fewer than 2^32
 
 inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }

@@ -175,7 +175,8 @@ def test_plan_refuses_overlaps(L):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(), WORKSPACE), (dict(ws=ODD, wsb=1 << 20), WORKSPACE), (dict(ws=FAKE, wsb=64), WORKSPACE), (dict(n=-1), INVALID),
-    (dict(n=1 << 31), UNSUPPORTED), (dict(G=0), INVALID), (dict(G=9000), UNSUPPORTED), (dict(bits=16), INVALID),
+    (dict(n=1 << 31), UNSUPPORTED), (dict(n=1 << 22), UNSUPPORTED), (dict(n=(1 << 22) - 1), WORKSPACE), (dict(G=0), INVALID),
+    (dict(G=9000), UNSUPPORTED), (dict(bits=16), INVALID),
     (dict(tiles=NULL), INVALID), (dict(first=NULL), INVALID), (dict(hyper=NULL), INVALID), (dict(hyper=ctypes.c_void_p(0x1004)), INVALID),
     (dict(steps=NULL), INVALID), (dict(active=ctypes.c_void_p(0x1002)), INVALID), (dict(norm=ctypes.c_void_p(0x1002)), INVALID)])
 def test_step(L, kw, status):
@@ -187,6 +188,16 @@ def test_step(L, kw, status):
 def test_step_workspace_bytes(L):
     f = L.lora_adamw_workspace_bytes
     assert f(0, 1) > 0 and f(1000, 3) >= 8000 and f(-1, 1) == 0 and f(5, 0) == 0 and f(1 << 31, 1) == 0 and f(5, 9000) == 0
+    assert f((1 << 22) - 1, 1) > 0 and f(1 << 22, 1) == 0
+
+
+def test_plan_refuses_more_tiles_than_a_launch_has(L):
+    """4,194,304 tiles of 1,024 threads are 2^32 threads: no launch has as many."""
+    n = 8200
+    ts = [tensor(1, 2 ** 21, 0, at=(i + 1) << 32) for i in range(n)]  # 512 tiles each
+    assert plan(L, ts, want=False)[0] == UNSUPPORTED
+    st, count, _, _ = plan(L, ts[:8191], want=False)
+    assert st == OK and count == 8191 * 512
 
 
 # ---- positions of several axes ----
