@@ -569,7 +569,8 @@ lora_status lora_layer_norm(const uint16_t* x, int64_t ldx, const uint16_t* resi
  *  - dweight, dbias float [K], or NULL where not wanted (written, not accumulated into; zero for
  *    T == 0), 16-byte aligned;
  *  - workspace: lora_layer_norm_backward_workspace_bytes(T, K) bytes, in any state, when dweight or
- *    dbias is wanted (partial sums, added in a fixed order: the result does not depend on timing). */
+ *    dbias is wanted (partial sums, added in a fixed order: the result does not depend on timing); calls
+ *    that overlap in time need their own. */
 lora_status lora_layer_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh,
                                      const float* weight, const uint16_t* dsum, int64_t ldds, int32_t T, int32_t K,
                                      float eps, int32_t rms, uint16_t* dx, int64_t lddx, float* dweight, float* dbias,
@@ -642,7 +643,7 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
  *    no clipping, and gradients that are not finite reach the states;
  *  - status device int32 or NULL (OR-ed in);
  *  - workspace: lora_adamw_workspace_bytes bytes, zero-filled once before first use (every call leaves
- *    its counters at zero again).
+ *    its counters at zero again); calls that overlap in time need their own.
  * A group without tensors makes no steps.  States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to
  * nearest even, and the scale largest / 448; blocks whose largest magnitude is below 2^-100 as zero;
  * a root of v that is not 0 keeps a code that is not (a code of 0 would let the next step grow to

@@ -5,6 +5,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <initializer_list>
 #include <limits>
 #include <stdexcept>
@@ -99,8 +100,9 @@ Rows rows(const Tensor& t, const char* name, int64_t width, int64_t T, const at:
   return {static_cast<uint16_t*>(t.data_ptr()), T > 1 ? t.stride(0) : width};
 }
 
+// A new tensor straight from the device's allocator (at::empty finds it through the dispatcher).
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 
 int32_t tokens(const Tensor& t, const char* name) {
