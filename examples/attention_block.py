@@ -6,7 +6,8 @@ projection to those after the output projection, with random weights:
 
 ``serve`` fills the cache with prompts, then verifies drafted trees: every round is one replay of a
 captured graph, after which one path of each tree is kept.  ``train`` runs the block's forward and
-backward over whole sequences and moves the adapters and norm weights.
+backward over whole sequences and moves the adapters and norm weights by gradient descent,
+``train_adamw`` by AdamW, each tenant by its own settings and only where it has tokens.
 
     python examples/attention_block.py [--kv bf16|fp8] [--rounds N]
 """
@@ -270,6 +271,35 @@ def train(block, x, target, ids, lens, steps=3, rate=1.0):
     return losses
 
 
+def train_adamw(block, x, target, ids, lens, steps=3, rate=1e-3, state_bits=8):
+    """The same by AdamW, one call a step for all adapters and norm weights: a tenant's gradients clipped
+    to norm 1, tenants without tokens left as they are.  The call leaves the adapters packed.  Returns
+    (losses, the step's handle)."""
+    n = block.qkv.ad.n
+    tensors, names = [], []
+    for p, name in ((block.qkv, "qkv"), (block.o, "o")):
+        for a in range(n):
+            tensors += [P.AdamWTensor(p.A[a], torch.zeros_like(p.A[a]), a, "A", p.ad.A[a], p.ad.At[a], p.bw.Ar[a]),
+                        P.AdamWTensor(p.B[a], torch.zeros_like(p.B[a]), a, "B", p.ad.B[a], p.ad.Bt[a], p.bw.Bop[a])]
+            names += [(name + "_A", a), (name + "_B", a)]
+    for name in ("q_weight", "k_weight"):  # of no tenant: a group of their own
+        w = getattr(block, name)
+        tensors.append(P.AdamWTensor(w, torch.zeros_like(w), n))
+        names.append((name, None))
+    opt = P.AdamW(tensors, n + 1, state_bits=state_bits)
+    hyper = torch.tensor([[rate, 0.9, 0.999, 1e-8, 0.01, 1.0]] * (n + 1), dtype=torch.float64, device="cuda")
+    active = torch.ones(n + 1, dtype=torch.int32, device="cuda")
+    losses = []
+    for _ in range(steps):
+        loss, g, _ = train_step(block, x, target, ids, lens)
+        losses.append(loss)
+        for t, (name, a) in zip(tensors, names):
+            t.grad.copy_(g[name] if a is None else g[name][a])
+        active[:n] = (torch.bincount(ids, minlength=n) > 0).int()
+        P.adamw_step(opt, hyper, active=active, clip=True)
+    return losses, opt
+
+
 def training_batch(block, lens, tenants, seed=3):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     T = sum(lens)
@@ -292,7 +322,10 @@ def main():
           f"status {status}, mean |y| {torch.cat(ys).float().abs().mean():.3f}", flush=True)
     block = AttentionBlock(1024, 8, 2, 128, ranks, max_pos=2048, train=True)
     lens = [100, 37, 1, 62]
-    print("training losses", [f"{v:.5f}" for v in train(block, *training_batch(block, lens, 4), lens)], flush=True)
+    batch = training_batch(block, lens, 4)
+    print("training losses", [f"{v:.5f}" for v in train(block, *batch, lens)], flush=True)
+    losses, _ = train_adamw(block, *batch, lens)
+    print("with AdamW", [f"{v:.5f}" for v in losses], flush=True)
 
 
 if __name__ == "__main__":
