@@ -366,10 +366,12 @@ __device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& 
   float4 g4[Q], p4[Q], m4[Q], v4[Q];
   uint32_t mc[Q], vc[Q];
   float ms[Q], vs[Q];
-  // all loads first; a lane without a quad reads the tile's first, since a load under a condition would
-  // wait for those before it
+  // Waves without a quad only take part in the barriers.  In the others all loads come first; a lane
+  // without a quad reads the tile's first, since a load under a condition would wait for those before it.
+  const bool idle = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~63) >= at.n4;
 #pragma unroll
   for (int k = 0; k < Q; ++k) {
+    if (idle) break;
     const int i = threadIdx.x + WG * k, n = i < at.n4 ? at.n - 4 * i : PART ? 0 : 4;
     const long o = at.at(i < at.n4 ? i : 0);
     if (BITS8) {
@@ -385,6 +387,7 @@ __device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& 
     p4[k] = ld4<PART, PAST>(t.param + o, n);
   }
   const Coef c = get_coef();
+  if (idle) return;
   const bool quads = t.cols % 4 == 0;
   const unsigned by_rank = (1u << 20) / (unsigned)max(1, min(t.cols, 64)) + 1;  // i / r of A, for i < 4096
 
