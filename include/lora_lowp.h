@@ -609,7 +609,7 @@ typedef struct lora_adamw_tensor {
   uint16_t* pack;         /* the packed forms of A and B (see above), whole, padding ranks included, */
   uint16_t* pack_bwd;     /*   or NULL                                                              */
   int32_t rows, cols;     /* A: K, r; B: r, N.  K % 64 == 0, N % 64 == 0, 1 <= r <= 64; any sizes for */
-  int32_t group;          /*   a plain tensor; rows cols < 2^31                                     */
+  int32_t group;          /*   a plain tensor; rows cols < 2^31 - 4096                              */
   int32_t kind;
 } lora_adamw_tensor;
 

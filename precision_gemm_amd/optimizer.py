@@ -22,6 +22,11 @@ from .ops import Adapters, BackwardAdapters, Grads, a_rows, rank_pad
 LORA_ADAMW_NOT_FINITE = 1
 _KIND = {"plain": 0, "A": 1, "B": 2}
 _BLOCK = 64
+_MOST_VALUES = 2**31 - 4097  # lora_adamw_tensor
+
+
+def _int32(n: int) -> bool:  # ctypes keeps the low bits of what is larger
+    return -2**31 <= n < 2**31
 
 
 @dataclass
@@ -80,6 +85,8 @@ class AdamW:
     def __init__(self, tensors: list, n_groups: int, *, state_bits: int = 32, steps: torch.Tensor | None = None):
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
+        if not _int32(n_groups):
+            raise ValueError(f"n_groups must be an int32, got {n_groups}")
         if not tensors:
             raise ValueError("a step needs a tensor at least")
         self.tensors, self.n_groups, self.state_bits = list(tensors), int(n_groups), state_bits
@@ -109,6 +116,10 @@ class AdamW:
         if t.kind not in _KIND:
             raise ValueError('kind must be "A", "B" or "plain"')
         n = t.param.numel()
+        if n > _MOST_VALUES:
+            raise ValueError(f"param has {n} values, and {_MOST_VALUES} at most are taken: give it in parts")
+        if not _int32(t.group):
+            raise ValueError(f"there is no group {t.group}")
         if t.kind == "plain":
             rows, cols = 1, n
             packs = (0, 0)

@@ -54,3 +54,21 @@ def test_status_is_raised(monkeypatch):
     monkeypatch.setattr(_binding, "binding", lambda: types.SimpleNamespace(layer_norm=lambda *a: 2))
     with pytest.raises(RuntimeError, match="lora_layer_norm failed with status 2"):
         P.layer_norm(torch.zeros(2, 64))
+
+
+class Large(torch.Tensor):
+    """A tensor that says it is on device 1, and has no memory behind it."""
+    device = property(lambda self: torch.device("cuda", 1))
+    is_cuda = property(lambda self: True)
+
+
+@pytest.mark.parametrize("n, group, n_groups, match", [
+    (2**32 + 64, 0, 1, "values"),             # of which 32 bits hold 64
+    (2**31 - 4096, 0, 1, "values"),
+    (64, 2**32, 1, "group"),                  # of which they hold 0
+    (64, 0, 2**32 + 1, "n_groups"),
+])
+def test_numbers_behind_32_bits(n, group, n_groups, match):
+    x = torch.empty(n, dtype=torch.float32, device="meta").as_subclass(Large)
+    with pytest.raises(ValueError, match=match):
+        P.AdamW([P.AdamWTensor(x, x, group)], n_groups)
