@@ -156,13 +156,15 @@ __global__ __launch_bounds__(WG) void k_norm(NormParams p) {
 // the next AHEAD of them in flight; a thread meets the same columns in every row, so it keeps their
 // weights, and their sums for the weights' gradients, in registers.  One workgroup a CU (256 in all), for
 // each leaves a row of partial sums (512: 20 % longer).  Sums meet a wave's lanes by DPP and its
-// workgroup's waves through LDS, three times a row; what would overlap badly across the barriers is few
-// instructions (24 a value).  4,096 rows of 4,096 values, with the residual stream's gradient (134 MB): 26.6 us, 5.0
-// TB/s, and k_norm_join.  Loads under a condition (which wait for the next row's): 36.
+// workgroup's waves through LDS, three times a row (twice for the RMS norm).  With the dot product taken
+// beside the squares, about h - mu and scaled afterwards, it is once less: 2 to 4 % faster up to 2,048
+// columns, 2 to 12 % slower from 8,192 on, where the registers are short.  4,096 rows of 4,096 values, with
+// the residual stream's gradient (134 MB): 26.6 us, 5.0 TB/s, and k_norm_join.  Loads under a condition
+// (which wait for the next row's): 36.
 template <int TPR, int C, int WG, int AHEAD, bool RMS, bool DSUM>
 __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
   constexpr int WAVES = TPR / 64, ROWS = WG / TPR;
-  __shared__ float red0[WG / 64][1], red1[WG / 64][1], red2[WG / 64][2];
+  __shared__ float red0[WG / 64][1], red1[WG / 64][1], red2[WG / 64][RMS ? 1 : 2];
   __shared__ __attribute__((aligned(16))) float join[ROWS > 1 ? (ROWS - 1) * TPR * C * 8 : 4];
   const int tid = threadIdx.x % TPR, group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const float inv = 1.0f / (float)p.K;
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
     }
     row_sum<WAVES, 1>(q, red1);
     const float r = 1.0f / sqrtf(q[0] * inv + p.eps);
-    float m[2] = {0.f, 0.f};
+    float m[RMS ? 1 : 2] = {};  // g xh, and g
     if (t < p.T) {  // a row behind the last is all zeros, whose r may be infinite
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -233,13 +235,13 @@ __global__ __launch_bounds__(WG) void k_norm_bwd(NormBwdParams p) {
           dw[c][e] += g[c][e] * h[c][e];
           db[c][e] += g[c][e];
           g[c][e] *= w[c][e];
-          m[0] += g[c][e];
-          m[1] += g[c][e] * h[c][e];
+          m[0] += g[c][e] * h[c][e];
+          if (!RMS) m[RMS ? 0 : 1] += g[c][e];
         }
       }
     }
-    row_sum<WAVES, 2>(m, red2);
-    const float m0 = RMS ? 0.f : m[0] * inv, m1 = m[1] * inv;
+    row_sum<WAVES, RMS ? 1 : 2>(m, red2);
+    const float m0 = RMS ? 0.f : m[RMS ? 0 : 1] * inv, m1 = m[0] * inv;
     const RowBuffer rx(p.dx, p.lddx, t, p.K, t < p.T);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
