@@ -644,10 +644,15 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
  *  - status device int32 or NULL (OR-ed in);
  *  - workspace: lora_adamw_workspace_bytes bytes, zero-filled once before first use (every call leaves
  *    its counters at zero again); calls that overlap in time need their own.
- * A group without tensors makes no steps.  States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to
- * nearest even, and the scale largest / 448; blocks whose largest magnitude is below 2^-100 as zero;
- * a root of v that is not 0 keeps a code that is not (a code of 0 would let the next step grow to
- * m / eps).  The step itself uses m and v before that rounding. */
+ * A group without tensors makes no steps.
+ * States in 8 bits: a block of 64 values is held as e4m3fn codes of value * (448 / largest), to nearest
+ * even, and the scale largest / 448, the largest of the block's finite magnitudes; blocks whose largest
+ * is below 2^-100 as zero; a root of v that is not 0 keeps a code that is not (a code of 0 would let the
+ * next step grow to m / eps).  The step itself uses m and v before that rounding.
+ * What is not finite in m or v (without norms, of a gradient that is not; and of one above 1.8e19, whose
+ * square is not) is the value's own: in 32 bits it is kept as it is, in 8 bits as the code of NaN, which
+ * makes the value itself NaN at its next step.  No other value is touched by it, except that codes are
+ * relative to the block's largest finite value, however large. */
 lora_status lora_adamw_step(const lora_adamw_tile* tiles, int64_t n_tiles, const int32_t* group_first, int32_t n_groups,
                             int32_t state_bits, const double* hyper, const int32_t* active, int32_t* steps,
                             float* grad_norm, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);

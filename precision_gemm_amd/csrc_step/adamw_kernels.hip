@@ -8,9 +8,9 @@
 // a step has one result whatever the compiler joins: an 8-bit state next to a border of its code
 // would otherwise depend on it.  Group coefficients are taken in 64 bits and rounded once.
 //
-// States in 8 bits: blocks of 64 values share a scale (the largest magnitude / 448); a value is an
-// e4m3 code.  Of v its root is held, which halves the exponents that a code has to span; a root that
-// is not 0 keeps a code that is not (0 would make the next step as large as m / eps).
+// States in 8 bits: blocks of 64 values share a scale (the largest finite magnitude / 448); a value is an
+// e4m3 code, NaN's for what is not finite.  Of v its root is held, which halves the exponents that a code
+// has to span; a root that is not 0 keeps a code that is not (0 would make the next step as large as m / eps).
 //
 // Bound by HBM: 59 instructions a value with states in 32 bits, 94 in 8, beside 28 and 16 bytes of
 // states and master copies and 6 of bf16 forms.  A workgroup takes a tile whose bf16 form it has in LDS,
@@ -32,7 +32,7 @@ enum { KIND_PLAIN = LORA_ADAMW_PLAIN, KIND_A = LORA_ADAMW_A, KIND_B = LORA_ADAMW
 // Values of a tile in LDS: of A, span rows of r + 4; of B, r rows of span + 8.
 constexpr int ADAMW_LDS = 5120;
 
-constexpr float E4M3_MAX = 448.f;
+constexpr float E4M3_MAX = 448.f, F32_MAX = 3.402823466e38f;
 constexpr float NO_SCALE = 0x1p-100f;  // blocks below it are held as zero: their scale's inverse would overflow
 
 // A tile's place: `n4` quads of values, quad i at value at(i) of the tensor.
@@ -279,20 +279,50 @@ __device__ __forceinline__ void values(uint32_t c, float scale, float (&v)[4]) {
   v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c, 2) * scale;
   v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c, 3) * scale;
 }
-// Scale of a block from its 16 lanes' quads (a row of lanes), and its inverse.
+// Largest magnitude of a block from its 16 lanes' quads (a row of lanes); NaN counts for nothing.
 template <int CTRL>
 __device__ __forceinline__ float row_max(float a) {
   return fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, a), CTRL, 0xf, 0xf, true)));
 }
-__device__ __forceinline__ void block_scale(const float (&v)[4], float& scale, float& inv) {
+__device__ __forceinline__ float block_max(const float (&v)[4]) {
   float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-  a = row_max<0xb1>(a);   // its neighbour
-  a = row_max<0x4e>(a);   // the other pair of four
-  a = row_max<0x141>(a);  // the other four of eight
-  a = row_max<0x140>(a);  // the other eight
-  a = a >= NO_SCALE ? a : 0.f;
+  a = row_max<0xb1>(a);          // its neighbour
+  a = row_max<0x4e>(a);          // the other pair of four
+  a = row_max<0x141>(a);         // the other four of eight
+  return row_max<0x140>(a);      // the other eight
+}
+// Scale of a block, and its inverse.
+__device__ __forceinline__ void block_scale(const float (&v)[4], float& scale, float& inv) {
+  float a = block_max(v);
+  a = a >= NO_SCALE ? a : 0.f;  // (of nothing but NaN: NaN, so 0)
   scale = a * (1.f / E4M3_MAX);
   inv = a > 0.f ? 1.f / a * E4M3_MAX : 0.f;
+}
+
+// A quad of its block's moments and roots as it is held in 8 bits.
+struct Held { float ms, vs; uint32_t m, v; };
+__device__ __forceinline__ Held hold(const float (&m)[4], const float (&root)[4]) {
+  Held h;
+  float inv, q[4];
+  block_scale(m, h.ms, inv);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = m[e] * inv;
+  h.m = codes(q);
+  block_scale(root, h.vs, inv);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    q[e] = root[e] * inv;
+    if (root[e] > 0.f && inv > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);  // the least code that is not 0
+  }
+  h.v = codes(q);
+  return h;
+}
+// What is infinite (of an infinite gradient, or of one whose square is) becomes NaN, which counts for
+// nothing in its block.
+__device__ __forceinline__ void no_infinity(float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (!(fabsf(v[e]) <= F32_MAX)) v[e] = __builtin_nanf("");
 }
 
 // Eight bf16 of the tile in LDS from (row, col) on, along its rows or its columns; the first n of
@@ -423,23 +453,21 @@ __device__ __forceinline__ void update(const lora_adamw_tensor& t, const Place& 
         for (int e = 0; e < 4; ++e)
           if (e >= n) m[e] = root[e] = 0.f;
       }
-      float sm, sv, inv, q[4];
-      block_scale(m, sm, inv);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = m[e] * inv;
-      const uint32_t cm = codes(q);
-      block_scale(root, sv, inv);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        q[e] = root[e] * inv;
-        if (root[e] > 0.f && inv > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);  // the least code that is not 0
+      Held h = hold(m, root);
+      // An infinite scale would make the whole block 0 * infinity at the next step.  Asked of the wave, so
+      // that a block's lanes stay together, and of the result, so that the scales need not wait for it (32
+      // tenants 179 us with it and without, odd ranks 18.4 and 18.0; asked before the codes 180 and 18.7).
+      if (__builtin_expect(__any(fmaxf(h.ms, h.vs) > F32_MAX), 0)) {
+        no_infinity(m);
+        no_infinity(root);
+        h = hold(m, root);
       }
       if (!live) continue;
-      st4<PART, false>(reinterpret_cast<uint8_t*>(t.m) + o, cm, n);
-      st4<PART, false>(reinterpret_cast<uint8_t*>(t.v) + o, codes(q), n);
+      st4<PART, false>(reinterpret_cast<uint8_t*>(t.m) + o, h.m, n);
+      st4<PART, false>(reinterpret_cast<uint8_t*>(t.v) + o, h.v, n);
       if ((threadIdx.x & 15) == 0) {
-        stg(t.m_scale + o / ADAMW_BLOCK, sm);
-        stg(t.v_scale + o / ADAMW_BLOCK, sv);
+        stg(t.m_scale + o / ADAMW_BLOCK, h.ms);
+        stg(t.v_scale + o / ADAMW_BLOCK, h.vs);
       }
     } else {
       if (!live) continue;
