@@ -78,8 +78,10 @@ def _check(t: torch.Tensor, name: str, dtype, numel: int, dev) -> int:
 class AdamW:
     """The tensors of a step with their states, cut into tiles once (lora_adamw_plan); the handle of
     :func:`adamw_step`.  ``steps`` int32 [n_groups] holds the steps that each group has made (zeros if
-    not given).  The handle holds the addresses of its tensors' buffers: gradients are written into
-    those (``lora_backward`` does), and adapters that are packed into new buffers need a new handle.
+    not given).  The handle holds the addresses of its tensors' buffers, and keeps their memory for as long
+    as it lives: gradients are written into those (``lora_backward`` does), and what a field or a tensor
+    of ``tensors`` is given in their place afterwards is not seen (a new handle is needed for it, as for
+    adapters that are packed into new buffers).
     Calls on one handle must be ordered on one stream: they share its states and workspace."""
 
     def __init__(self, tensors: list, n_groups: int, *, state_bits: int = 32, steps: torch.Tensor | None = None):
@@ -93,6 +95,8 @@ class AdamW:
         if not isinstance(self.tensors[0].param, torch.Tensor) or not self.tensors[0].param.is_cuda:
             raise ValueError("param must be a device tensor")
         dev = self.device = self.tensors[0].param.device
+        # memory whose addresses the plan holds: the tensors' fields are the caller's, who may replace them
+        self._memory = []
         structs = (AdamWTensorStruct * len(self.tensors))()
         for t, s in zip(self.tensors, structs):
             self._fill(t, s, dev)
@@ -155,6 +159,8 @@ class AdamW:
                 if not size:
                     raise ValueError(f"{name} is for A and B")
                 setattr(s, name, _check(b, name, torch.bfloat16, size, dev))
+        self._memory += [b.untyped_storage() for b in (t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.pack, t.pack_bwd)
+                         if b is not None]
         s.rows, s.cols, s.group, s.kind = rows, cols, t.group, _KIND[t.kind]
 
 
