@@ -13,7 +13,7 @@ int32_t width(const Tensor& t, const char* name) {
   return (int32_t)t.size(1);
 }
 
-// x, weight, bias, residual, eps, rms, out, sum_out, stream -> (y, h)
+// x, weight, bias, residual, eps, rms, out, sum_out, stream -> (y, h), h None where y has taken its place
 PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
     const Tensor& x = req(a[0], "x");
@@ -34,6 +34,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (res) rs = rows(h, "sum_out", K, T, dev);
     const lora_status s = lora_layer_norm(rx.p, rx.ld, rr.p, rr.ld, T, K, w, b, eps, rms, ry.p, ry.ld, rs.p, rs.ld, stream(a[8]));
     if (s != LORA_OK) return status(s);
+    if (!res && T > 0 && ry.p == rx.p) return Py_BuildValue("(NO)", THPVariable_Wrap(y), Py_None);
     return Py_BuildValue("(NN)", THPVariable_Wrap(y), THPVariable_Wrap(h));
   });
 }

@@ -18,7 +18,8 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, *, residual=None, eps: f
     """Norm of each row of ``x`` (lora_layer_norm), bf16 [T, K], rows of any stride; ``rms`` without
     the mean.  ``weight`` and ``bias`` float32 [K] or None.  With ``residual`` (as ``x``) the norm is of
     h = bf16(x + residual).  Returns ``(y, h)``, bf16 [T, K], h being ``x`` itself without a residual;
-    in ``out`` and ``sum_out`` if given, which may be ``x`` or ``residual``."""
+    in ``out`` and ``sum_out`` if given, which may be ``x`` or ``residual``.  Without a residual, ``out=x``
+    leaves no h for :func:`layer_norm_backward`: None is returned in its place."""
     return call("layer_norm", x, x, weight, bias, residual, eps, rms, out, sum_out)
 
 

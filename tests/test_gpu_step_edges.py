@@ -178,3 +178,40 @@ def test_axes_with_most_tokens():
     q, k = P.qk_norm_rope(qkv, pos, 1, 1, 64, **args)
     a, b = P.qk_norm_rope(qkv[-100:].contiguous(), pos[:, -100:].contiguous(), 1, 1, 64, **args)
     assert torch.equal(q[-100:], a) and torch.equal(k[-100:], b)
+
+
+@pytest.mark.parametrize("T,K,rms,extra", [(5, 64, False, 0), (16, 4096, True, 8), (1, 520, False, 0)])
+def test_norm_over_its_input_has_no_h(T, K, rms, extra):
+    """Without a residual h is x itself: where y takes x's place there is none, and the backward, which needs
+    it, refuses what is returned in its place."""
+    import torch
+    import precision_gemm_amd as P
+    print("[case] norm in place", T, K, rms, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((T, K + extra), generator=g, device="cuda").bfloat16()[:, :K]
+    other = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    want, h = P.layer_norm(x, rms=rms)
+    assert h is x
+    y, h = P.layer_norm(x, rms=rms, out=other)
+    assert h is x and y is other and torch.equal(y, want)
+    # the other half of one buffer's rows is another place
+    both = torch.cat([x, x], 1)
+    y, h = P.layer_norm(both[:, :K], rms=rms, out=both[:, K:])
+    assert torch.equal(h, x) and torch.equal(both[:, K:], want) and torch.equal(both[:, :K], x)
+    y, h = P.layer_norm(x, rms=rms, out=x)
+    assert h is None and y.data_ptr() == x.data_ptr() and torch.equal(x, want)
+    with pytest.raises(ValueError, match="h must be a tensor"):
+        P.layer_norm_backward(y, h, rms=rms)
+    # with a residual h is the sum, in a place of its own
+    r = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    s = (x.float() + r.float()).bfloat16()
+    y, h = P.layer_norm(x, residual=r, rms=rms, out=x)
+    assert torch.equal(h, s) and torch.equal(x, P.layer_norm(s, rms=rms)[0])
+
+
+def test_norm_over_its_input_without_rows():
+    import torch
+    import precision_gemm_amd as P
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    y, h = P.layer_norm(x, out=x)
+    assert y.shape == (0, 64) and (h is None or h.shape == (0, 64))
