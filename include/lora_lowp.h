@@ -553,8 +553,8 @@ lora_status lora_rope_axes_append_kv(const uint16_t* qkv, int64_t ld, const int3
  *  - y bf16 [T] rows of K (ldy); sum: h, bf16 (lds), with a residual, else NULL.  y and sum may be
  *    the rows of x or of the residual, each of them whole and in its own place; any other overlap is
  *    not allowed.
- * Statistics are those of the stored (rounded) h, in fp32, the squares summed about the mean; y is
- * rounded once. */
+ * Statistics are those of the stored (rounded) h, in fp32, the squares summed about the mean (the sum has
+ * to fit: for values up to 1e17); y is rounded once. */
 lora_status lora_layer_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, int32_t T, int32_t K,
                             const float* weight, const float* bias, float eps, int32_t rms, uint16_t* y, int64_t ldy,
                             uint16_t* sum, int64_t lds, void* stream);
@@ -632,15 +632,16 @@ lora_status lora_adamw_plan(const lora_adamw_tensor* tensors, int32_t n, int32_t
 
 /* One step.
  *  - tiles, group_first: from lora_adamw_plan, in device memory; state_bits 32 or 8, as there;
- *  - hyper double [n_groups][6]: rate, beta1, beta2, eps, weight decay, largest gradient norm (0 or
- *    less: not clipped);
+ *  - hyper double [n_groups][6]: rate, beta1, beta2 (each 0 or more, below 1), eps, weight decay,
+ *    largest gradient norm (0 or less: not clipped);
  *  - active int32 [n_groups] or NULL: groups that are 0 here are left as they are (a tenant without
  *    tokens in the batch);
  *  - steps int32 [n_groups]: the steps that each group has made, counted on by the groups that step;
  *  - grad_norm float [n_groups] or NULL.  With it, each active group's gradient norm (fp64 sums in a
- *    fixed order) is written there (0 for the others), gradients are clipped by it, and a group whose
- *    norm is not finite is left as it was, with LORA_ADAMW_NOT_FINITE in *status.  Without it there is
- *    no clipping, and gradients that are not finite reach the states;
+ *    fixed order) is written there (0 for the others; infinity where it passes fp32's range), gradients
+ *    are clipped by it, and a group whose norm is not finite in fp64 is left as it was, with
+ *    LORA_ADAMW_NOT_FINITE in *status.  Without it there is no clipping, and gradients that are not
+ *    finite reach the states (below);
  *  - status device int32 or NULL (OR-ed in);
  *  - workspace: lora_adamw_workspace_bytes bytes, zero-filled once before first use (every call leaves
  *    its counters at zero again); calls that overlap in time need their own.

@@ -12,11 +12,11 @@
 // e4m3 code, NaN's for what is not finite.  Of v its root is held, which halves the exponents that a code
 // has to span; a root that is not 0 keeps a code that is not (0 would make the next step as large as m / eps).
 //
-// Bound by HBM: 59 instructions a value with states in 32 bits, 94 in 8, beside 28 and 16 bytes of
+// Bound by HBM: 59 instructions a value with states in 32 bits, 95 in 8, beside 28 and 16 bytes of
 // states and master copies and 6 of bf16 forms.  A workgroup takes a tile whose bf16 form it has in LDS,
 // so that the packed forms, one of which is always across the tensor's rows, leave in whole 16-byte
 // pieces in the same pass (repacking by launches of their own would be two for each adapter).  32 tenants of rank 16
-// on four projections (35.7 million values, 1.21 GB; 0.79 in 8 bits): 195 us, 6.2 TB/s, and 152, 5.2; a
+// on four projections (35.7 million values, 1.21 GB; 0.79 in 8 bits): 195 us, 6.2 TB/s, and 147, 5.4; a
 // copy of as many bytes reaches 5.1.
 #include <algorithm>
 
@@ -546,18 +546,25 @@ __global__ __launch_bounds__(WG) void k_adamw(AdamWParams p) {
 // Steps of few tiles without norms are one launch.  Each arrival at a group's counter takes about 13 ns,
 // one behind another where all tiles are one group's, and goes on beside the other tiles' work: 80 tiles
 // 6.8 us with a launch for the groups, 6.1 without; 304 in 8 bits 13.0 and 12.0; 992 of one group 28.4
-// and 28.4; 816 of small tiles 18.3 and 18.7.
+// and 28.4; 816 of small tiles 18.3 and 18.7 (about even from 800 tiles on).
 constexpr long ALONE_TILES = 1024;
 
 // With norms, the groups of so few tiles are settled in the norms' launch by the same arrivals (32 tiles
 // 11.7 us with a launch for the groups, 9.6 without; 80 12.0 and 10.9; 304 of one group 17.0 and 19.5).
+// What makes it slower is many arrivals at one group's counter: the rule counts all tiles, as if they were
+// one group's, and where they are many groups' it gives up its gain sooner than it would have to.
 constexpr long LAST_TILES = 128;
 
-// Steps of more tiles than this (8 million values, 250 MB and more) read and write their states and
-// master copies past the caches, which could not hold them until the next step: what the norms'
-// launch has read of the gradients then stays for the update (the layer above: 265 us within them, 237
-// past them, with norms).  Codes and scales of 8-bit states stay within: a wave's 256 bytes are too
-// short for it (188 us with all within the caches, 180 with the master copies past them, 190 with all).
+// Steps of more tiles than this read and write their states and master copies past the caches, which
+// could not hold them until the next step: what the norms' launch has read of the gradients then stays
+// for the update (the layer above: 265 us within them, 237 past them, with norms).  Codes and scales of
+// 8-bit states stay within: a wave's 256 bytes are too short for it (188 us with all within the caches,
+// 180 with the master copies past them, 190 with all).  Full tiles, as many as this, are
+// 8 million values: about 185 MB with gradients and packed forms, 135 in 8 bits.  Tiles of small ranks hold
+// fewer (512 values of rank 1), and a step of theirs would fit the caches.  With other work between two
+// steps (1 GiB copied before each) it is the same to them: 32 tenants of rank 1 without norms 51 us past the
+// caches and 51 within, in 8 bits 55 and 55, of rank 4 69 and 69 (63 and 63).  Steps one right behind another
+// lose by it: 48 and 40 us of rank 1, 50 and 43 in 8 bits; of rank 8 in 8 bits (8.9 million values) 52 and 47.
 constexpr long STREAM_TILES = 2048;
 
 constexpr int WG = 1024;

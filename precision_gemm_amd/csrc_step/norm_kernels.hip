@@ -387,7 +387,10 @@ hipError_t launch_norm(const NormParams& p, bool rms, hipStream_t s) {
 // of 512 in workgroups of 512 threads 11.3 us, of 1,024 11.8, of 256 12.4; of 2,048 (128 threads, 2 chunks,
 // 4 rows 23.2; 256 x 1, 4 rows 24.0); 4,096 of 4,096 (256 x 2, 2 rows 30.2, two rows ahead 30.2; 512 x 1,
 // 2 rows 31.1); 1,001 of 5,376 (384 x 2, 2 rows 13.1; 512 x 2 15.6); 4,096 of 8,192 (1024 x 1 49.7; 512 x 2
-// 50.9); 2,048 of 16,384 (512 x 4 66; 1024 x 2 spills, 89).
+// 50.9); 2,048 of 16,384 (512 x 4 66; 1024 x 2 spills, 89), whose form also takes 8,200 columns and more
+// (4,096 rows of 8,200 73.9 us, of 10,240 77.1, of 12,288 84.5; 768 x 2 73.9, 77.1 and 85.7).  Without the
+// weights' gradients the sums are kept all the same, and no k_norm_join follows: 4,096 of 4,096 25.8 us
+// where both take 31.8 and one 30.1.
 hipError_t launch_norm_bwd(const NormBwdParams& p, bool rms, hipStream_t s) {
   if (p.K <= 512) return launch_bwd<64, 1, 512, 1>(p, rms, s);
   if (p.K <= 1024) return launch_bwd<128, 1, 512, 1>(p, rms, s);

@@ -33,8 +33,8 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight=None, *, dsum=
                         workspace=None):
     """Gradients of :func:`layer_norm` (lora_layer_norm_backward): ``dy`` bf16 [T, K] and ``h`` as the
     forward returned it -> ``(dx, dweight, dbias)``: bf16 [T, K], the gradient of ``x`` and of
-    ``residual`` alike, and float32 [K], None where ``weight_grad`` or ``bias_grad`` is False.  ``dsum``
-    is the gradient that reaches h along the residual stream, added to ``dx`` (which may be its buffer,
-    or ``dy``'s).  Output buffers and the workspace (calls that overlap in time need their own) may be
+    ``residual`` alike, and float32 [K], None where ``weight_grad`` or ``bias_grad`` is False
+    (frozen weights, an RMS norm without a bias: each of the two takes time of its own).  ``dsum`` is the
+    gradient that reaches h along the residual stream, added to ``dx`` (which may be its buffer, or ``dy``'s).  Output buffers and the workspace (calls that overlap in time need their own) may be
     passed in; then the call allocates nothing."""
     return call("layer_norm_backward", dy, dy, h, weight, dsum, eps, rms, weight_grad, bias_grad, dx, dweight, dbias, workspace)
