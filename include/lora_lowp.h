@@ -562,7 +562,8 @@ lora_status lora_layer_norm(const uint16_t* x, int64_t ldx, const uint16_t* resi
 /* Gradients of lora_layer_norm.  With g = dy w, r = 1 / sqrt(mean((h - mu)^2) + eps), xh = (h - mu) r:
  *     dx = r (g - mean(g) - xh mean(g xh)) + dsum   (without mean(g) for rms = 1)
  *     dweight = sum over the rows of dy xh,  dbias = sum of dy
- *  - dy bf16 [T] rows of K (lddy); h bf16 (ldh): the forward's sum, or its x without a residual;
+ *  - dy bf16 [T] rows of K (lddy); h bf16 (ldh): the forward's sum, or its x without a residual (which
+ *    a y in its place has overwritten);
  *  - dsum bf16 (ldds) or NULL: the gradient that reaches h along the residual stream;
  *  - dx bf16 (lddx): the gradient of x, and of the residual alike.  It may be dy's or dsum's rows in
  *    their own places;

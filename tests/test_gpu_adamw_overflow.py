@@ -68,13 +68,11 @@ def _check(c, before, clip):
 
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("beta1", [0.9, 0.0])
-@pytest.mark.parametrize("clip", [False, True])
-@pytest.mark.parametrize("bad", VALUES)
+@pytest.mark.parametrize("bad,clip", [(b, c) for b, v in VALUES.items() for c in ((False, True) if np.isfinite(v) else (False,))])
 def test_no_other_value_is_touched(bad, clip, beta1, bits):
-    """Also with norms, where the largest norm of 0 takes finite gradients as they are."""
+    """Also with norms, where the largest norm of 0 takes finite gradients as they are (with others a group
+    makes no step)."""
     import torch
-    if clip and not np.isfinite(VALUES[bad]):
-        pytest.skip("with norms such a group makes no step")
     print("[case] overflow", bad, clip, beta1, bits, flush=True)
     c = Case(SHAPES, 3, bits, 11)
     c.hyper[:, 1], c.hyper[:, 5] = beta1, 0.0
